@@ -250,7 +250,7 @@ def _prepare_decode(case, seed):
         st["cache"] = bdfp8.FP8Cache(k_pages, v_pages, st["kv_scales"], P, hkv, d, fmt)
         st["chunk"] = bdfp8.bdfp8_decode_plan(lens, tq, hq, hkv, d, torch.cuda.get_device_properties(0).multi_processor_count,
                                               window=case["window"], sinks=case["sinks"])
-        st["workspace"] = bdfp8.workspace_for(B, tq, hq, d, mp, st["chunk"], window=case["window"], sinks=case["sinks"])
+        st["workspace"] = bdfp8.workspace_for(B, tq, hq, hkv, d, mp, st["chunk"], window=case["window"], sinks=case["sinks"])
         st["out"] = torch.empty_like(st["q"])
     return st
 
