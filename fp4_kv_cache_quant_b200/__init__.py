@@ -3,4 +3,4 @@
 ``bdfp4`` is the ctypes binding of the CUDA library ``libbdfp4.so`` (C ABI in
 ``include/bdfp4.h``); ``workloads`` draws seeded synthetic inputs.
 """
-from . import bdfp4, workloads  # noqa: F401
+from . import bdfp4, bdfp8, workloads  # noqa: F401

@@ -1,0 +1,332 @@
+// append_fp8.cu -- appending keys and values to the 8-bit paged cache (bdfp8.h)
+// with the position rotation of keys and queries on the way.
+//
+// One CTA per (block of 16 tokens that the call touches, KV head): D threads for
+// the keys (a row's 16 elements each), D for the values (a channel each), and all
+// of them for the rotation of the group's queries.  The work is moving bytes
+// (2 B in, 1 B out per key and value element, 2 + 2 per query element); a block's
+// scale needs its maximum first, so its elements wait in registers.
+//
+// Which sequence a CTA serves: sequence b gets the item numbers f(b) .. f(b+1) - 1,
+// f(b) = cu[b] / 16 + 2 b.  n tokens from any offset touch at most n / 16 + 2 blocks
+// (rounded down), which that leaves room for, so f needs no prefix sum: a warp
+// finds b by a 32-way search of cu_tokens.
+
+#include <climits>
+
+#include "decode_common.cuh"
+#include "fp8_device.cuh"
+#include "host_common.h"
+
+namespace bdfp4 {
+namespace fp8 {
+
+struct AppendArgs {
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* q_out;
+    int64_t k_stride, v_stride, q_stride;
+    const int32_t* cu;
+    const int32_t* seq_lens;
+    const int32_t* positions;
+    const float* cos_sin;
+    float* k_open;
+    __nv_bfloat16* v_open;
+    const int32_t* block_table;
+    uint8_t* k_pages;
+    uint8_t* v_pages;
+    float* kv_scales;
+    int32_t* dev_status;
+    int64_t num_pages;
+    int B, T, H_q, H_kv, G, rot, max_pos, adjacent, max_pages;
+};
+
+// x cos - y sin to the nearest fp32 but for the last step's rounding: both products' and the
+// difference's errors are kept, so that a code does not depend on how fp32 happened to round.
+__device__ __forceinline__ float turn(float x, float c, float y, float s) {
+    const float p = __fmul_rn(x, c), ep = __fmaf_rn(x, c, -p);
+    const float q = __fmul_rn(y, s), eq = __fmaf_rn(y, s, -q);
+    const float t = __fsub_rn(p, q);
+    const float bb = __fsub_rn(t, p);
+    const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(t, bb)), -__fadd_rn(q, bb));
+    return __fadd_rn(t, __fadd_rn(e, __fsub_rn(ep, eq)));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(p));
+}
+
+// Elements e0 .. e0 + 7 of a row rotated by `cs` (rot / 2 cosines, then as many sines; null = not rotated).
+template <bool EXACT>
+__device__ __forceinline__ void rotated8(const __nv_bfloat16* row, int e0, const float* cs, int rot, bool adjacent,
+                                         float* x) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(row + e0)), x);
+    if (!cs || e0 >= rot) return;
+    auto comb = [](float a, float c, float b, float s) { return EXACT ? turn(a, c, b, s) : fmaf(a, c, -(b * s)); };
+    const int half = rot >> 1;
+    if (adjacent) {
+        float c[4], s[4];
+        load4(cs + (e0 >> 1), c);
+        load4(cs + half + (e0 >> 1), s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = comb(a, c[i], b, s[i]);
+            x[2 * i + 1] = comb(b, c[i], a, -s[i]);
+        }
+    } else {
+        const bool lower = e0 < half;
+        const int f = lower ? e0 : e0 - half;
+        float y[8], c[8], s[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(row + (lower ? e0 + half : e0 - half))), y);
+        load4(cs + f, c);
+        load4(cs + f + 4, c + 4);
+        load4(cs + half + f, s);
+        load4(cs + half + f + 4, s + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = comb(x[i], c[i], y[i], lower ? s[i] : -s[i]);
+    }
+}
+
+// The smallest power of two s >= 2^-126 with amax <= top s, as its exponent; top = 1.75 2^L.
+template <int FMT>
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+    constexpr int L = FMT == BDFP8_E4M3 ? 8 : 15;
+    const int e = (int)(amax_bits >> 23) - 127 - L + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax_bits == 0 ? 0 : max(e, -126);
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
+    constexpr int WK = D / 32;             // warps of the keys, and of the values
+    constexpr int PAGE = kPageSlots * D;
+    __shared__ uint32_t red[2][WK];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int item = blockIdx.x / a.H_kv, hk = blockIdx.x % a.H_kv;
+
+    if (blockIdx.x == 0)   // the sequences that are left out
+        for (int b = tid; b < a.B; b += 2 * D) {
+            const int c0 = a.cu[b], c1 = a.cu[b + 1], N = a.seq_lens[b];
+            if (c0 < 0 || c1 < c0 || c1 > a.T || N < c1 - c0 || N > a.max_pages * kPageSlots)
+                set_status(a.dev_status, BDFP4_DEV_BAD_SEQLEN);
+        }
+
+    // the last b with cu[b] / 16 + 2 b <= item
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) >> 5;
+        const int at = lo + lane * step;
+        const bool le = at < hi && (lane == 0 || (__ldg(a.cu + at) >> 4) + 2 * at <= item);
+        const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    const int b = lo;
+    const int c0 = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - c0, end = __ldg(a.seq_lens + b);
+    if (n <= 0 || c0 < 0 || c0 > a.T - n || end < n || end > a.max_pages * kPageSlots) return;
+    const int start = end - n;
+    const int blk0 = start / kBlockTokens, last = (end - 1) / kBlockTokens;
+    const int mine = blk0 + item - ((c0 >> 4) + 2 * b);
+    if (mine < blk0 || mine > last) return;
+
+    // table row of token t's position (null: not rotated)
+    auto angles = [&](int t, int index) -> const float* {
+        if (a.rot == 0) return nullptr;
+        const int pos = a.positions ? __ldg(a.positions + t) : index;
+        if (pos < 0 || pos >= a.max_pos) {
+            set_status(a.dev_status, BDFP8_DEV_BAD_POSITION);
+            return nullptr;
+        }
+        return a.cos_sin + (int64_t)pos * a.rot;
+    };
+
+    // Blocks of this CTA: its own; and, where the sequence's first block has open rows and is not its last,
+    // the first block's CTA does the last one too, after it has read the open rows that the last one replaces.
+    const bool reads_open = start % kBlockTokens != 0;
+    const bool chained = reads_open && last != blk0;
+    for (int blk = mine;;) {
+        if (!(chained && mine == last)) {
+            const int i0 = blk * kBlockTokens;                 // first token index of the block
+            const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + i0 / kPageSlots);
+            const bool page_ok = page >= 0 && page < a.num_pages;
+            if (!page_ok && tid == 0) set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
+            const int64_t ph = (int64_t)page * a.H_kv + hk;
+            const int slot0 = i0 % kPageSlots;
+            const bool is_v = tid >= D;
+            float x[16];
+            uint32_t mx = 0;
+            if (!is_v) {
+                // keys: row tid / (D / 16), elements 16 c .. 16 c + 15
+                const int r = tid / (D / 16), c = tid % (D / 16), i = i0 + r;
+                const int64_t open = (((int64_t)b * kBlockTokens + r) * a.H_kv + hk) * D + 16 * c;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+                if (i < start) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(a.k_open + open + e);
+                } else if (i < end) {
+                    const int t = c0 + i - start;
+                    const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
+                    const float* cs = angles(t, i);
+                    rotated8<true>(row, 16 * c, cs, a.rot, a.adjacent, x);
+                    rotated8<true>(row, 16 * c + 8, cs, a.rot, a.adjacent, x + 8);
+                    if (blk == last) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(a.k_open + open + e) = *reinterpret_cast<const float4*>(x + e);
+                    }
+                }
+            } else {
+                // values: channel tid - D, one register per token
+                const int ch = tid - D;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int i = i0 + r;
+                    __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + r) * a.H_kv + hk) * D + ch;
+                    if (i < start) {
+                        x[r] = __bfloat162float(*open);
+                    } else if (i < end) {
+                        const __nv_bfloat16 w = a.v[(int64_t)(c0 + i - start) * a.v_stride + hk * D + ch];
+                        x[r] = __bfloat162float(w);
+                        if (blk == last) *open = w;
+                    } else {
+                        x[r] = 0.0f;
+                    }
+                }
+            }
+            // as bits, a NaN is above an infinity and that above every number
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            if (lane == 0) red[is_v][warp % WK] = mx;
+            __syncthreads();
+            mx = red[is_v][0];
+#pragma unroll
+            for (int w = 1; w < WK; ++w) mx = max(mx, red[is_v][w]);
+            const int e = scale_exp<FMT>(mx);
+            const float inv = pow2i(-e);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = f8x2<FMT>(x[4 * i] * inv, x[4 * i + 1] * inv) | (f8x2<FMT>(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+            if (page_ok) {
+                uint8_t* dst;
+                if (!is_v) {
+                    const int s = slot0 + tid / (D / 16);
+                    dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (tid % (D / 16)) * 128 + (s & 7) * 16;
+                } else {
+                    const int ch = tid - D;
+                    dst = a.v_pages + ph * PAGE + (ch >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (ch & 7) * 16;
+                }
+                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (tid == 0 || tid == D)
+                    a.kv_scales[ph * kScalePage + (is_v ? kBlocksPerPage : 0) + slot0 / kBlockTokens] =
+                        mx >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : pow2i(e);
+            }
+        }
+        if (!(chained && blk == blk0)) break;
+        blk = last;
+        __syncthreads();   // the open rows of the first block are read, its maxima too
+    }
+
+    // queries of the group: 8 elements per thread and step
+    if (a.q) {
+        const int i0 = max(mine * kBlockTokens, start), i1 = min((mine + 1) * kBlockTokens, end);
+        const int per = a.G * (D / 8);
+        for (int u = tid; u < (i1 - i0) * per; u += 2 * D) {
+            const int i = i0 + u / per, w = u % per, t = c0 + i - start;
+            const int h = hk * a.G + w / (D / 8), e0 = w % (D / 8) * 8;
+            float x[8];
+            rotated8<false>(a.q + t * a.q_stride + h * D, e0, angles(t, i), a.rot, a.adjacent, x);
+            uint4 o;
+            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                ow[e] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            *reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * a.H_q + h) * D + e0) = o;
+        }
+    }
+}
+
+}  // namespace fp8
+}  // namespace bdfp4
+
+using namespace bdfp4;
+using namespace bdfp4::fp8;
+
+extern "C" int bdfp8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                            int64_t q_stride, void* q_out, const int32_t* cu_tokens, const int32_t* seq_lens,
+                            const int32_t* positions, const float* cos_sin, int rot_dim, int max_pos, int pairing,
+                            float* k_open, void* v_open, const int32_t* block_table, int B, int T, int H_q, int H_kv,
+                            int d, int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, void* k_pages,
+                            void* v_pages, float* kv_scales, int32_t* dev_status, void* stream) {
+    if (B < 0 || T < 0 || H_q <= 0 || H_kv <= 0 || max_pages_per_seq <= 0 || num_pages < 0 || max_pos < 0 || rot_dim < 0 ||
+        (fmt != BDFP8_E4M3 && fmt != BDFP8_E5M2) || (pairing != BDFP8_ROTATE_HALVES && pairing != BDFP8_ROTATE_ADJACENT) ||
+        !q != !q_out)
+        return BDFP4_ERR_ARG;
+    if (H_q % H_kv || rot_dim > d || rot_dim % 16 || k_stride < (int64_t)H_kv * d || v_stride < (int64_t)H_kv * d ||
+        (q && q_stride < (int64_t)H_q * d))
+        return BDFP4_ERR_SHAPE;
+    if (d != 64 && d != 128) return BDFP4_ERR_UNSUPPORTED;
+    const int64_t ctas = ((int64_t)T / kBlockTokens + 2 * (int64_t)B) * H_kv;
+    if (max_pages_per_seq > (1 << 24) || num_pages > INT_MAX || ctas > INT_MAX || (int64_t)T + 32LL * B > INT_MAX)
+        return BDFP4_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return BDFP4_OK;
+    if (!k || !v || !cu_tokens || !seq_lens || !k_open || !v_open || !block_table || !k_pages || !v_pages || !kv_scales ||
+        (rot_dim > 0 && !cos_sin))
+        return BDFP4_ERR_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) ||
+        !aligned(k_open, 128) || !aligned(v_open, 128) || !aligned(k_pages, 128) || !aligned(v_pages, 128) ||
+        !aligned(kv_scales, 128) || k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
+        return BDFP4_ERR_ALIGN;
+    AppendArgs a{};
+    a.k = (const __nv_bfloat16*)k;
+    a.v = (const __nv_bfloat16*)v;
+    a.q = (const __nv_bfloat16*)q;
+    a.q_out = (__nv_bfloat16*)q_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.cu = cu_tokens;
+    a.seq_lens = seq_lens;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.k_open = k_open;
+    a.v_open = (__nv_bfloat16*)v_open;
+    a.block_table = block_table;
+    a.k_pages = (uint8_t*)k_pages;
+    a.v_pages = (uint8_t*)v_pages;
+    a.kv_scales = kv_scales;
+    a.dev_status = dev_status;
+    a.num_pages = num_pages;
+    a.B = B;
+    a.T = T;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.G = H_q / H_kv;
+    a.rot = rot_dim;
+    a.max_pos = max_pos;
+    a.adjacent = pairing == BDFP8_ROTATE_ADJACENT;
+    a.max_pages = max_pages_per_seq;
+    cudaStream_t st = (cudaStream_t)stream;
+    const unsigned grid = (unsigned)ctas;
+    if (fmt == BDFP8_E4M3) {
+        if (d == 128) append_fp8_kernel<BDFP8_E4M3, 128><<<grid, 256, 0, st>>>(a);
+        else append_fp8_kernel<BDFP8_E4M3, 64><<<grid, 128, 0, st>>>(a);
+    } else {
+        if (d == 128) append_fp8_kernel<BDFP8_E5M2, 128><<<grid, 256, 0, st>>>(a);
+        else append_fp8_kernel<BDFP8_E5M2, 64><<<grid, 128, 0, st>>>(a);
+    }
+    return launch_status();
+}

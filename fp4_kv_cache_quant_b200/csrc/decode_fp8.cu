@@ -1,0 +1,867 @@
+// decode_fp8.cu -- decode attention over the 8-bit paged cache (bdfp8.h), to the
+// whole context or through a sliding window with visible first tokens.
+//
+// The mathematics.  With codes k', v' and block scales a_t (keys), c_t (values),
+// out = sum_t p_t c_t v'_t / sum_t p_t, p_t = exp(sm_scale a_t q.k'_t - m).  The
+// tensor cores multiply 8-bit floats, so the cache's bytes are MMA operands as they
+// stand and only the two small factors are split to fit:
+//  - q = (q1 + q2 / 16) / 2^s: two E4M3 terms.  A bf16 element has 8 significant
+//    bits, an E4M3 term 4, and the rest after rounding to 4 bits fits 4 bits: exact
+//    for elements down to 2^-13 of the row's largest.
+//  - p c = (P1 + P2 + P3) 2^(e-15): three E5M2 terms of what the earlier ones leave.
+//    Each keeps 3 bits (relative error 2^-9 after three, bf16's own 2^-9 on average)
+//    and their common floor is 2^-32 of the largest p c, so a sink with a million
+//    faint tokens behind it keeps their mass (E4M3 terms would be finer, 2^-12, but
+//    end at 2^-26).  2^e bounds the value scales seen so far.
+// The terms are stacked as columns of one MMA (N = 2 rows of q, 3 rows of P), S^T =
+// K q^T with M = 128 tokens and O^T = V^T P^T with M = 128 channels.
+//
+// One CTA per (sequence, KV head, group of up to 32 stacked query rows, split):
+// eight softmax warps in two groups that each own half of the rows (thread = token,
+// then thread = channel), a producer warp (bulk copies into a key and a value ring;
+// keys run one tile ahead) and an MMA warp.  Query rows are the G T_q (token, head)
+// rows of the KV head.
+//
+// A row group's tiles are those of the first `sinks` tokens and those from its oldest
+// window token on, numbered one after another and cut into splits, so a window
+// costs what it shows, wherever it stands.
+
+#include <algorithm>
+#include <climits>
+
+#include "decode_common.cuh"
+#include "fp8_device.cuh"
+#include "host_common.h"
+
+namespace bdfp4 {
+namespace fp8 {
+
+struct Args {
+    const __nv_bfloat16* q;
+    const uint8_t* k_pages;
+    const uint8_t* v_pages;
+    const float* kv_scales;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    float* ws_o;    // [B T_q H_q][max_splits][d] unnormalised partial outputs
+    float* ws_ml;   // [B T_q H_q][max_splits][2] (m in log2 units, l)
+    __nv_bfloat16* out;
+    int32_t* dev_status;
+    int B, T_q, H_q, H_kv, G, max_pages, window, sinks, chunk_tiles, max_splits, groups;
+    int64_t num_pages;
+    float sm_scale;
+};
+
+// The tiles that rows r0 .. r1 of a KV head's stacked rows see (row r is query token r / G).
+struct Tiles {
+    int end;      // tokens from here on are seen by none of the rows
+    int lo;       // first token of the oldest window (0 without a window)
+    int front;    // tiles of the first tokens, before the window's tiles
+    int first;    // first tile of the window
+    int total;
+    __device__ __forceinline__ int tile(int v) const { return v < front ? v : first + v - front; }
+};
+
+__device__ __forceinline__ Tiles tiles_of(int N, int T_q, int G, int r0, int r1, int window, int sinks) {
+    Tiles t;
+    t.end = max(0, N - T_q + r1 / G + 1);
+    t.lo = window > 0 ? max(0, N - T_q + r0 / G - window + 1) : 0;
+    t.lo = min(t.lo, t.end);
+    const int last = (t.end + kTileTokens - 1) / kTileTokens;
+    t.first = t.lo / kTileTokens;
+    t.front = window > 0 ? min((min(sinks, t.end) + kTileTokens - 1) / kTileTokens, t.first) : 0;
+    t.total = t.front + last - t.first;
+    return t;
+}
+
+__device__ __forceinline__ int splits_of(const Tiles& t, int chunk) { return (t.total + chunk - 1) / chunk; }
+
+// A length out of range counts as an empty sequence.
+__device__ __forceinline__ int checked_len(const Args& a, int b) {
+    const int N = a.seq_lens[b];
+    return N < 0 || N > a.max_pages * kPageSlots ? 0 : N;
+}
+
+template <int FMT, int D, int ROWS, bool MT>
+struct Cfg {
+    static constexpr int NQ = 2 * ROWS < 16 ? 16 : 2 * ROWS;      // N of QK: q1 and q2 columns
+    static constexpr int NP = (3 * ROWS + 15) / 16 * 16;          // N of PV: three probability terms
+    static constexpr int KS = D / 32;                             // MMA K steps of QK
+    static constexpr int NSG = 2;                                 // softmax groups of four warps
+    static constexpr int HG = ROWS / NSG;                         // rows per group
+    static constexpr int HB = HG < 8 ? HG : 8;                    // rows handled at once
+    static constexpr int NSW = 4 * NSG;
+    static constexpr int PRODUCER = NSW, MMA_WARP = NSW + 1;
+    static constexpr int THREADS = 32 * (NSW + 2);
+    // Up to eight rows an SM holds three blocks of two 16 KB key and two value stages (192 KB in flight).
+    static constexpr int CTAS = ROWS <= 8 ? 3 : (ROWS == 16 ? 2 : 1);
+    static constexpr int NSK = CTAS == 3 ? 2 : 3, NSV = CTAS == 1 ? 3 : 2;
+    static constexpr int NSC = NSK <= 2 ? 4 : 8;                  // scale slots (at least NSK + 2, see the producer)
+    static constexpr int PAGE = kPageSlots * D;
+    static constexpr int TILE = 2 * PAGE;
+    static constexpr int P_BUF = NP * kTileTokens;                // [row/8][token/16][row%8][16]
+    static constexpr int SM_K = 0;
+    static constexpr int SM_V = SM_K + NSK * TILE;
+    // D = 64: the value MMA's M = 128 rows run 4 KB past a page, into the bytes that follow the
+    // ring; those products land in TMEM lanes that nothing reads
+    static constexpr int SM_P = SM_V + NSV * TILE;
+    static constexpr int SM_Q = SM_P + 2 * P_BUF;
+    static constexpr int SM_SC = SM_Q + NQ * D;                                // [NSC][2 pages][8] scales
+    static constexpr int RED_Q = ROWS + 2;                                    // a quadrant's maxima: rows, scale of each group
+    static constexpr int SM_RED = SM_SC + NSC * 2 * kScalePage * 4;           // [2][4][RED_Q]
+    static constexpr int SM_VM = (SM_RED + 2 * 4 * RED_Q * 4 + 15) / 16 * 16;   // [2][NSG][4] masks of visible tokens
+    static constexpr int SM_LSC = SM_VM + 2 * NSG * 16;                       // [ROWS] logit factors
+    static constexpr int SM_POK = SM_LSC + ROWS * 4;                          // [NSC] page flags
+    static constexpr int SM_BARS = (SM_POK + NSC * 4 + 7) / 8 * 8;
+    static constexpr int NBARS = 2 * NSK + 2 * NSV + 7;
+    static constexpr int SM_MISC = SM_BARS + NBARS * 8;
+    static constexpr int SMEM = SM_MISC + 16;
+    static_assert(2 * P_BUF >= 4096, "the value MMA's overrun at D = 64 stays inside the block's memory");
+    static_assert(SMEM <= 233472 / CTAS - 1024, "shared memory");
+    static_assert(NSC >= NSK + 2, "scale slots");
+    static constexpr int T_S = 0;                                 // TMEM columns: S^T double buffer, O^T
+    static constexpr int T_O = 2 * NQ;
+    static constexpr int T_USED = T_O + NP;
+    static constexpr int T_ALLOC = T_USED <= 64 ? 64 : (T_USED <= 128 ? 128 : 256);
+    static_assert(T_USED <= 256 && T_ALLOC * CTAS <= 512, "tensor memory");
+};
+
+constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
+
+template <int FMT, int D, int ROWS, bool MT>
+__global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, ROWS, MT>::CTAS)
+    decode_fp8_kernel(const Args a) {
+    using C = Cfg<FMT, D, ROWS, MT>;
+    constexpr int HG = C::HG, HB = C::HB;
+    // the split merge (a programmatic dependent) may be scheduled as CTAs of this grid retire
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* const p_op = smem + C::SM_P;
+    uint8_t* const q_op = smem + C::SM_Q;
+    float* const sc_ring = reinterpret_cast<float*>(smem + C::SM_SC);
+    float* const red = reinterpret_cast<float*>(smem + C::SM_RED);
+    uint32_t* const vmask = reinterpret_cast<uint32_t*>(smem + C::SM_VM);
+    float* const lsc = reinterpret_cast<float*>(smem + C::SM_LSC);
+    int* const pok = reinterpret_cast<int*>(smem + C::SM_POK);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);
+    uint64_t* const kfull = bars;
+    uint64_t* const kempty = kfull + C::NSK;
+    uint64_t* const vfull = kempty + C::NSK;
+    uint64_t* const vempty = vfull + C::NSV;
+    uint64_t* const s_full = vempty + C::NSV;   // [2] QK done, and the tile's scales seen -> softmax
+    uint64_t* const p_ready = s_full + 2;       // [2] P written, dead value columns zeroed -> MMA
+    uint64_t* const o_full = p_ready + 2;       // [2] PV done -> softmax
+    uint64_t* const q_ready = o_full + 2;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SM_MISC);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::SM_MISC + 4);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // row groups of one split stand next to each other: they read the same tiles
+    const int64_t cta = blockIdx.x;
+    const int rg = (int)(cta % a.groups);
+    const int64_t c1 = cta / a.groups;
+    const int split = (int)(c1 % a.max_splits);
+    const int64_t c2 = c1 / a.max_splits;
+    const int hk = (int)(c2 % a.H_kv), b = (int)(c2 / a.H_kv);
+    const int r0 = rg * ROWS, nrows = min(ROWS, a.G * a.T_q - r0);
+
+    const int N = checked_len(a, b);
+    const Tiles tl = tiles_of(N, a.T_q, a.G, r0, r0 + nrows - 1, a.window, a.sinks);
+    const int nspl = splits_of(tl, a.chunk_tiles);
+    if (tid == 0 && split == 0 && rg == 0 && hk == 0 && (N != a.seq_lens[b] || (N > 0 && N < a.T_q)))
+        set_status(a.dev_status, BDFP4_DEV_BAD_SEQLEN);
+    // row of the [B][T_q][H_q] arrays of stacked row r
+    auto row_of = [&](int r) -> int64_t {
+        return ((int64_t)b * a.T_q + r / a.G) * a.H_q + (int64_t)hk * a.G + r % a.G;
+    };
+    if (split > 0 && split >= nspl) return;
+    if (tl.total == 0) {
+        for (int i = tid; i < nrows * D; i += C::THREADS) a.out[row_of(r0 + i / D) * D + i % D] = __float2bfloat16(0.0f);
+        return;
+    }
+    const int tile0 = split * a.chunk_tiles;
+    const int n = min(a.chunk_tiles, tl.total - tile0);   // tiles of this split (>= 1)
+
+    if (tid == 0) {
+        for (int s = 0; s < C::NSK; ++s) {
+            tc::mbar_init(&kfull[s], 1);
+            tc::mbar_init(&kempty[s], 1);
+        }
+        for (int s = 0; s < C::NSV; ++s) {
+            tc::mbar_init(&vfull[s], 1);
+            tc::mbar_init(&vempty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&s_full[i], 2);   // the MMAs' commit, and the MMA lane itself
+            tc::mbar_init(&p_ready[i], C::NSW);
+            tc::mbar_init(&o_full[i], 1);
+        }
+        tc::mbar_init(q_ready, C::NSW);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == C::MMA_WARP) {
+        tc::tmem_alloc(tmem_slot, C::T_ALLOC);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+
+    if (warp == C::PRODUCER) {
+        // ------------------------------------------------------------ producer
+        // Step k issues the keys and scales of tile k and the values of tile k - 1, so keys run a
+        // tile ahead.  Lanes read the page ids of 32 tiles at once; one lane per copy issues.
+        // Scales go to slot k % NSC with the keys' byte count.  A key stage is refilled once its QK
+        // has completed, and the MMA lane issues QK of tile t only after p_ready of tile t - 2: when
+        // tile k's keys are issued, the softmax is done with the scales of tile k - NSK - 2, and
+        // with NSC >= NSK + 2 slot k % NSC is free.
+        bool ok = true;
+        int pv[2] = {-1, -1};
+        int k_last = -1, v_last = -1;
+        for (int j0 = 0; ok && j0 <= n; j0 += 32) {
+            int pg_l[2] = {-1, -1};
+            if (j0 + lane < n) {
+                const int tile = tl.tile(tile0 + j0 + lane);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int pi = tile * 2 + p, t0 = pi * kPageSlots;
+                    // pages that no row sees are not looked up
+                    if (t0 < tl.end && (t0 + kPageSlots > tl.lo || t0 < a.sinks)) {
+                        const int v = a.block_table[(int64_t)b * a.max_pages + pi];
+                        if (v >= 0 && v < a.num_pages) pg_l[p] = v;
+                        else set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
+                    }
+                }
+            }
+            const int kmax = min(32, n + 1 - j0);
+            for (int kk = 0; kk < kmax; ++kk) {
+                const int k = j0 + kk, v = k - 1;
+                int pk[2];
+                pk[0] = __shfl_sync(0xffffffffu, pg_l[0], kk);
+                pk[1] = __shfl_sync(0xffffffffu, pg_l[1], kk);
+                if (k < n) {
+                    const int s = k % C::NSK;
+                    if (lane == 0) {
+                        if (k >= C::NSK && !tc::mbar_wait(&kempty[s], ((k / C::NSK) - 1) & 1, abort_flag, kWaitLimit)) {
+                            ok = false;
+                        } else {
+                            pok[k % C::NSC] = (pk[0] >= 0 ? 1 : 0) | (pk[1] >= 0 ? 2 : 0);
+                            tc::mbar_arrive_expect_tx(&kfull[s], ((pk[0] >= 0) + (pk[1] >= 0)) * (C::PAGE + kScalePage * 4));
+                        }
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if (lane < 4) {
+                        const int p = lane & 1, pg = pk[p];
+                        const int64_t ph = (int64_t)pg * a.H_kv + hk;
+                        if (pg >= 0) {
+                            if (lane < 2)
+                                tc::bulk_g2s(smem + C::SM_K + s * C::TILE + p * C::PAGE, a.k_pages + ph * C::PAGE, C::PAGE,
+                                             &kfull[s]);
+                            else
+                                tc::bulk_g2s(sc_ring + ((k % C::NSC) * 2 + p) * kScalePage, a.kv_scales + ph * kScalePage,
+                                             kScalePage * 4, &kfull[s]);
+                        }
+                    }
+                    k_last = k;
+                }
+                if (v >= 0) {
+                    const int s = v % C::NSV;
+                    if (lane == 0) {
+                        if (v >= C::NSV && !tc::mbar_wait(&vempty[s], ((v / C::NSV) - 1) & 1, abort_flag, kWaitLimit))
+                            ok = false;
+                        else
+                            tc::mbar_arrive_expect_tx(&vfull[s], ((pv[0] >= 0) + (pv[1] >= 0)) * C::PAGE);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if (lane < 2 && pv[lane] >= 0)
+                        tc::bulk_g2s(smem + C::SM_V + s * C::TILE + lane * C::PAGE,
+                                     a.v_pages + ((int64_t)pv[lane] * a.H_kv + hk) * C::PAGE, C::PAGE, &vfull[s]);
+                    v_last = v;
+                }
+                pv[0] = pk[0];
+                pv[1] = pk[1];
+            }
+        }
+        if (!ok && lane == 0) *abort_flag = 1;
+        // unwinding: every copy this warp started lands before the CTA can exit
+        if ((!ok || *abort_flag) && lane == 0) {
+            for (int s = 0; s < C::NSK; ++s)
+                if (k_last >= s)
+                    tc::mbar_wait_drain(&kfull[s], ((k_last - (k_last - s) % C::NSK) / C::NSK) & 1, kWaitLimit);
+            for (int s = 0; s < C::NSV; ++s)
+                if (v_last >= s)
+                    tc::mbar_wait_drain(&vfull[s], ((v_last - (v_last - s) % C::NSV) / C::NSV) & 1, kWaitLimit);
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_f8(Fmt8<FMT>::mma, Fmt8<BDFP8_E4M3>::mma, C::NQ);
+            constexpr uint32_t idesc_pv = idesc_f8(Fmt8<FMT>::mma, Fmt8<BDFP8_E5M2>::mma, C::NP);
+            const uint32_t q_addr = tc::smem_u32(q_op);
+            const uint32_t p_addr = tc::smem_u32(p_op);
+            const uint32_t k_addr = tc::smem_u32(smem + C::SM_K);
+            const uint32_t v_addr = tc::smem_u32(smem + C::SM_V);
+            // the last commit: its phase completes once every tcgen05 operation issued before it has
+            uint64_t* last_bar = nullptr;
+            uint32_t last_par = 0;
+            auto issue_qk = [&](int j) -> bool {
+                const int s = j % C::NSK, buf = j & 1;
+                if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, kWaitLimit)) return false;
+                tc::tc_fence_after();
+                const uint32_t kt = k_addr + s * C::TILE;
+                // key rows: 8-row groups 8 D bytes apart (SBO), 16-element chunks 128 bytes apart (LBO)
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks)
+                    mma_f8(tbase + C::T_S + buf * C::NQ, tc::smem_desc(kt + ks * 256, 128, 8 * D),
+                           tc::smem_desc(q_addr + ks * 256, 128, 8 * D), idesc_qk, ks > 0);
+                tc::mma_commit(&s_full[buf]);
+                tc::mma_commit(&kempty[s]);
+                // passes on this thread's view of the copied scales and the page flags
+                tc::mbar_arrive(&s_full[buf]);
+                last_bar = &kempty[s];
+                last_par = (uint32_t)(j / C::NSK) & 1u;
+                return true;
+            };
+            bool ok = tc::mbar_wait(q_ready, 0, abort_flag, kWaitLimit);
+            if (ok) tc::tc_fence_after();
+            ok = ok && issue_qk(0);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n && !(ok = issue_qk(j + 1))) break;
+                const int s = j % C::NSV, buf = j & 1;
+                if (!(ok = tc::mbar_wait(&p_ready[buf], (j >> 1) & 1, abort_flag, kWaitLimit))) break;
+                if (!(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit))) break;
+                tc::tc_fence_after();
+                const uint32_t vt = v_addr + s * C::TILE;
+                // V^T: 8-channel groups 512 bytes apart, 16-slot chunks 128 apart; P: 8-row groups 1 KB
+                // apart.  O^T accumulates over the split's tiles (the softmax warps rescale it).
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_f8(tbase + C::T_O, tc::smem_desc(vt + (ks >> 1) * C::PAGE + (ks & 1) * 256, 128, 512),
+                           tc::smem_desc(p_addr + buf * C::P_BUF + ks * 256, 128, 1024), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
+                tc::mma_commit(&o_full[buf]);
+                tc::mma_commit(&vempty[s]);
+                last_bar = &vempty[s];
+                last_par = (uint32_t)(j / C::NSV) & 1u;
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                // the tensor memory is freed below: the MMAs into it must have finished
+                if (last_bar) tc::mbar_wait_drain(last_bar, last_par, kWaitLimit);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax warps
+        const int grp = warp >> 2;
+        const int qd = warp & 3;                   // TMEM lane quadrant: tokens 32 qd .. 32 qd + 31 of a tile
+        const int gb = grp * HG;                   // first row of the group
+        const int bar_id = 1 + grp;
+        const uint32_t tq = tbase + ((uint32_t)(32 * qd) << 16);
+        bool bad = false, grp_abort = false;
+
+        // query rows as two E4M3 terms: q 2^(7-e) in [128, 256) for the row's largest, the rest times 16
+        for (int r = warp; r < ROWS; r += C::NSW) {
+            constexpr int E = D / 32;              // elements per lane
+            float x[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = 0.0f;
+            if (r < nrows) {
+                const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(a.q + row_of(r0 + r) * D) + lane * (E / 2);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const float2 f = __bfloat1622float2(src[i]);
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                }
+            }
+            // the largest exponent field of the row (255: an infinity or a NaN)
+            uint32_t ex = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) ex = max(ex, (__float_as_uint(x[i]) >> 23) & 0xffu);
+            ex = __reduce_max_sync(0xffffffffu, ex);
+            const int e = min(max((int)ex - 127, -119), 127);
+            const float up = pow2i(7 - e);
+            uint32_t c1w = 0, c2w = 0;
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                const float y0 = x[i] * up, y1 = x[i + 1] * up;
+                const uint32_t c = f8x2<BDFP8_E4M3>(y0, y1);
+                const float2 v = tc::e4m3x2_value(c);
+                c1w |= c << (8 * i);
+                c2w |= f8x2<BDFP8_E4M3>((y0 - v.x) * 16.0f, (y1 - v.y) * 16.0f) << (8 * i);
+            }
+            const int col = 2 * HG * (r / HG) + r % HG;   // a group's q1 columns, then its q2 columns
+            const int e0 = lane * E;
+            auto put = [&](int c, uint32_t w) {
+                uint8_t* dst = q_op + (c >> 3) * (8 * D) + (e0 >> 4) * 128 + (c & 7) * 16 + (e0 & 15);
+                if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = w;
+                else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
+            };
+            put(col, c1w);
+            put(col + HG, c2w);
+            // a row with an infinity or a NaN gives NaN logits
+            if (lane == 0) lsc[r] = ex == 255u ? __uint_as_float(0x7fc00000u) : a.sm_scale * kLog2e * pow2i(e - 7);
+        }
+        tc::fence_proxy_async_smem();
+        tc::named_bar_sync(1 + C::NSG, 32 * C::NSW);
+        if (lane == 0) tc::mbar_arrive(q_ready);
+
+        // The running maximum of row gb + hl lives in lanes hl, hl + HG, ... of the group's warps, which
+        // compute its terms once; the warp takes them by shuffle.  ev: 2^ev bounds the value scales
+        // seen so far (alike in all threads).
+        const int hl = lane % HG;
+        float m_l = -INFINITY;
+        int ev = -110;
+        float l_part[HG];
+#pragma unroll
+        for (int g = 0; g < HG; ++g) l_part[g] = 0.0f;
+        const int pg = qd >> 1;                                // page of this thread's token in the tile
+        const int blk = 2 * (qd & 1) + (lane >> 4);            // its scale block in the page
+        const int tok = 32 * qd + lane;
+        const int chan = tok;                                  // O^T lane = value channel
+        uint8_t* const pslot = p_op + (tok >> 4) * 128 + (tok & 15);
+        const uint32_t t_o = tq + C::T_O + 3 * gb;             // a group's first, second and third terms
+
+        for (int j = 0; j < n; ++j) {
+            const int buf = j & 1, t0 = tl.tile(tile0 + j) * kTileTokens;
+            if (!tc::mbar_wait(&s_full[buf], (j >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+            tc::tc_fence_after();
+            const float* sc = sc_ring + ((j % C::NSC) * 2 + pg) * kScalePage + blk;
+            const float ka = sc[0], va = sc[kBlocksPerPage];
+            const int t = t0 + tok;
+            const bool valid = t < tl.end && (t >= tl.lo || t < a.sinks) && ((pok[j % C::NSC] >> pg) & 1);
+            // several query tokens: row r sees t iff r / G >= t - (N - T_q) and, in a window, r / G < t + W - (N - T_q)
+            // or t < sinks: rows [vis0, vis1) of the group
+            [[maybe_unused]] int vis0 = 0, vis1 = HG;
+            if constexpr (MT) {
+                const int d = t - (N - a.T_q);
+                vis0 = min(max(d, 0), a.T_q) * a.G - r0 - gb;
+                if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - r0 - gb;
+            }
+            float x[HG];
+            float* const rw = red + (buf * 4 + qd) * C::RED_Q;
+#pragma unroll
+            for (int g0 = 0; g0 < HG; g0 += HB) {
+                uint32_t s1[HB], s2[HB];
+                tc::tmem_ld<HB>(tq + C::T_S + buf * C::NQ + 2 * gb + g0, s1);
+                tc::tmem_ld<HB>(tq + C::T_S + buf * C::NQ + 2 * gb + HG + g0, s2);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int g = 0; g < HB; ++g) {
+                    const float s = fmaf(__uint_as_float(s2[g]), 0.0625f, __uint_as_float(s1[g])) * ka * lsc[gb + g0 + g];
+                    const bool see = valid && (!MT || (g0 + g >= vis0 && g0 + g < vis1));
+                    x[g0 + g] = see ? s : -INFINITY;
+                }
+            }
+            float wm_l = -INFINITY;   // lane hl keeps row hl's maximum over the warp's tokens
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                const float wm = tc::redux_max_f32(x[g], 0xffffffffu);
+                wm_l = hl == g ? wm : wm_l;
+            }
+            const float vs = valid ? fabsf(va) : 0.0f;
+            const float vmx = tc::redux_max_f32(vs, 0xffffffffu);
+            const uint32_t seen = __ballot_sync(0xffffffffu, valid);
+            if (lane < HG) rw[gb + lane] = wm_l;
+            if (lane == 0) {
+                rw[ROWS + grp] = vmx;
+                vmask[(buf * C::NSG + grp) * 4 + qd] = seen;
+            }
+            // one decision for the group's four warps, taken by the barrier itself
+            if (tc::named_bar_or(bar_id, 128, bad)) {
+                grp_abort = true;
+                break;
+            }
+            const float* const rr = red + buf * 4 * C::RED_Q;
+            const float mt = fmaxf(fmaxf(rr[gb + hl], rr[C::RED_Q + gb + hl]),
+                                   fmaxf(rr[2 * C::RED_Q + gb + hl], rr[3 * C::RED_Q + gb + hl]));
+            const float vt = fmaxf(fmaxf(rr[ROWS + grp], rr[C::RED_Q + ROWS + grp]),
+                                   fmaxf(rr[2 * C::RED_Q + ROWS + grp], rr[3 * C::RED_Q + ROWS + grp]));
+            const uint4 vm = *reinterpret_cast<const uint4*>(vmask + (buf * C::NSG + grp) * 4);
+            const float mn = fmaxf(m_l, mt);
+            const float mz = mn == -INFINITY ? 0.0f : mn;
+            const float corr_l = tc::ex2_approx(m_l - mz);   // 0 before the first visible token
+            // the smallest exponent with |scale| <= 2^ev over what has been seen
+            const int en = max(ev, min((int)((__float_as_uint(vt) + 0x7fffffu) >> 23) - 127, 127));
+            const float down = pow2i(max(ev - en, -126));
+            const bool rose = __any_sync(0xffffffffu, mn != m_l || en != ev);
+            m_l = mn;
+            ev = en;
+            // value scale in units of 2^(ev - 15); nothing of a token that no row sees goes in
+            const float vy = valid ? va * pow2i(-en) * 32768.0f : 0.0f;
+            uint8_t* const pb = pslot + buf * C::P_BUF;
+#pragma unroll
+            for (int g = 0; g < HG; g += 2) {
+                constexpr int H1 = HG > 1 ? 1 : 0;
+                const float p0 = tc::ex2_approx(x[g] - __shfl_sync(0xffffffffu, mz, g));
+                const float p1 = tc::ex2_approx(x[g + H1] - __shfl_sync(0xffffffffu, mz, g + H1));
+                l_part[g] = fmaf(l_part[g], __shfl_sync(0xffffffffu, corr_l, g), p0);
+                l_part[g + H1] = fmaf(l_part[g + H1], __shfl_sync(0xffffffffu, corr_l, g + H1), p1);
+                // three E5M2 terms of p c: each leaves what it cannot hold (exact in fp16) to the next.
+                // An E5M2 code is the upper byte of the fp16 with its value.
+                __half2 y = __floats2half2_rn(p0 * vy, p1 * vy);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint16_t c;
+                    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t*>(&y)));
+                    const int r = 3 * gb + k * HG + g;
+                    pb[(r >> 3) * 1024 + (r & 7) * 16] = (uint8_t)c;
+                    pb[((r + H1) >> 3) * 1024 + ((r + H1) & 7) * 16] = (uint8_t)(c >> 8);
+                    if (k < 2) {
+                        const uint32_t back = __byte_perm((uint32_t)c, 0u, 0x1404);
+                        y = __hsub2(y, *reinterpret_cast<const __half2*>(&back));
+                    }
+                }
+            }
+            // O^T of the group's rows moves to the new maximum (and scale bound) once the previous
+            // tile's PV has completed, before this tile's PV is issued
+            if (j > 0 && rose) {
+                if (!tc::mbar_wait(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t ov[HG];
+                    tc::tmem_ld<HG>(t_o + k * HG, ov);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < HG; ++g)
+                        ov[g] = __float_as_uint(__uint_as_float(ov[g]) * (__shfl_sync(0xffffffffu, corr_l, g) * down));
+                    tc::tmem_st_n<HG>(t_o + k * HG, ov);
+                }
+                tc::tmem_wait_st();
+            }
+            // Value columns of tokens that no row sees are zeroed: their bytes may be anything (a NaN code
+            // among them), and 0 times NaN is NaN.  One channel per thread of group 0.
+            if (grp == 0 && (vm.x & vm.y & vm.z & vm.w) != 0xffffffffu) {
+                const int s = j % C::NSV;
+                if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit)) bad = true;
+                const uint32_t w[4] = {vm.x, vm.y, vm.z, vm.w};
+                if (chan < D) {
+                    uint8_t* const vc = smem + C::SM_V + s * C::TILE + (chan >> 3) * 512 + (chan & 7) * 16;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t m = (w[c >> 1] >> (16 * (c & 1))) & 0xffffu;
+                        if (m == 0xffffu) continue;
+                        uint4* const at = reinterpret_cast<uint4*>(vc + (c >> 2) * C::PAGE + (c & 3) * 128);
+                        auto bytes = [](uint32_t m4) { return (((m4 & 15u) * 0x00204081u) & 0x01010101u) * 0xffu; };
+                        uint4 v = *at;
+                        v.x &= bytes(m);
+                        v.y &= bytes(m >> 4);
+                        v.z &= bytes(m >> 8);
+                        v.w &= bytes(m >> 12);
+                        *at = v;
+                    }
+                }
+            }
+            tc::tc_fence_before();
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&p_ready[buf]);
+        }
+        // ------------------------------------------------------------ epilogue (thread = channel)
+        uint32_t o1[HG], o2[HG], o3[HG];
+        if (!grp_abort) {
+            if (!tc::mbar_wait(&o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+            tc::tc_fence_after();
+            tc::tmem_ld<HG>(t_o, o1);
+            tc::tmem_ld<HG>(t_o + HG, o2);
+            tc::tmem_ld<HG>(t_o + 2 * HG, o3);
+            tc::tmem_wait_ld();
+        }
+        grp_abort = tc::named_bar_or(bar_id, 128, grp_abort || bad || *abort_flag);
+        if (grp_abort) *abort_flag = 1;
+        if (!grp_abort) {
+            float* const rl = red;   // [4][RED_Q] partial sums (the maxima are no longer read)
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                float v = l_part[g];
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                if (lane == 0) rl[qd * C::RED_Q + gb + g] = v;
+            }
+            tc::named_bar_sync(bar_id, 128);
+            const float unit = pow2i(max(ev - 15, -126));
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                const int r = gb + g;
+                const float m_g = __shfl_sync(0xffffffffu, m_l, g);
+                if (r >= nrows || chan >= D) continue;
+                const float l = (rl[r] + rl[C::RED_Q + r]) + (rl[2 * C::RED_Q + r] + rl[3 * C::RED_Q + r]);
+                const float o = ((__uint_as_float(o3[g]) + __uint_as_float(o2[g])) + __uint_as_float(o1[g])) * unit;
+                const int64_t row = row_of(r0 + r);
+                if (nspl == 1) {
+                    a.out[row * D + chan] = __float2bfloat16(l == 0.0f ? 0.0f : o / l);
+                } else {
+                    a.ws_o[(row * a.max_splits + split) * D + chan] = o;
+                    if (chan == 0) {
+                        a.ws_ml[(row * a.max_splits + split) * 2] = m_g;
+                        a.ws_ml[(row * a.max_splits + split) * 2 + 1] = l;
+                    }
+                }
+            }
+        }
+    }
+
+    tc::tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && tid == 0) set_status(a.dev_status, BDFP4_DEV_TIMEOUT);
+    if (warp == C::MMA_WARP) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tbase, C::T_ALLOC);
+    }
+}
+
+// Log-sum-exp merge of the splits, one warp per output row (64 or 128 channels):
+//   out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
+// A split whose tokens a row does not see has m = -inf, l = 0 and weight 0; a NaN among the
+// sums reaches the output.
+template <int D>
+__global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_per_cta) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.B * a.T_q * a.H_q) return;
+    const int64_t bt = row / a.H_q;
+    const int h = (int)(row % a.H_q), b = (int)(bt / a.T_q), i = (int)(bt % a.T_q);
+    const int r = i * a.G + h % a.G, r0 = r / rows_per_cta * rows_per_cta;
+    const Tiles tl = tiles_of(checked_len(a, b), a.T_q, a.G, r0, min(r0 + rows_per_cta, a.G * a.T_q) - 1, a.window, a.sinks);
+    const int ns = splits_of(tl, a.chunk_tiles);
+    if (ns <= 1) return;   // written by the decode kernel
+    const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.max_splits;
+    float M = -INFINITY;
+    for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[s].x);
+    M = tc::redux_max_f32(M, 0xffffffffu);
+    if (M == -INFINITY) M = 0.0f;
+    constexpr int E = D / 32;
+    float acc[E], L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    const float* o = a.ws_o + row * a.max_splits * D + lane * E;
+#pragma unroll 4
+    for (int s = 0; s < ns; ++s) {
+        const float2 w2 = ml[s];
+        const float w = exp2f(w2.x - M);
+        L = fmaf(w2.y, w, L);
+        float v[E];
+        if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o + (int64_t)s * D);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o + (int64_t)s * D);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// ------------------------------------------------------------------ host
+inline int rows_for(int G, int64_t T_q) {
+    const int64_t rows = G * T_q;
+    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+inline int ctas_per_sm(int rows) { return rows <= 8 ? 3 : rows == 16 ? 2 : 1; }
+
+// Most tiles that a row group of a sequence of at most N tokens can see.
+inline int64_t most_tiles(int64_t N, int T_q, int G, int rows, int window, int sinks) {
+    const int64_t all = (N + kTileTokens - 1) / kTileTokens;
+    if (window <= 0) return all;
+    // the group's query tokens: their windows span window + span - 1 tokens from any slot on
+    const int64_t span = std::min<int64_t>(T_q, (rows - 1) / G + 2);
+    const int64_t win = (window + span - 1 + kTileTokens - 2) / kTileTokens + 1;
+    return std::min(all, win + (sinks + kTileTokens - 1) / kTileTokens);
+}
+
+template <int FMT, int D, int ROWS, bool MT>
+static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
+    using C = Cfg<FMT, D, ROWS, MT>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return BDFP4_ERR_CUDA;
+    }
+    decode_fp8_kernel<FMT, D, ROWS, MT><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
+    const int rc = launch_status();
+    if (rc != BDFP4_OK || a.max_splits <= 1) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.T_q * a.H_q + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, merge_fp8_kernel<D>, a, ROWS);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return BDFP4_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+template <int FMT, int D>
+static int dispatch(const Args& a, int rows, int64_t ctas, cudaStream_t st) {
+    if (a.T_q > 1) {
+        switch (rows) {
+            case 4: return launch<FMT, D, 4, true>(a, ctas, st);
+            case 8: return launch<FMT, D, 8, true>(a, ctas, st);
+            case 16: return launch<FMT, D, 16, true>(a, ctas, st);
+            default: return launch<FMT, D, 32, true>(a, ctas, st);
+        }
+    }
+    switch (rows) {
+        case 4: return launch<FMT, D, 4, false>(a, ctas, st);
+        case 8: return launch<FMT, D, 8, false>(a, ctas, st);
+        case 16: return launch<FMT, D, 16, false>(a, ctas, st);
+        default: return launch<FMT, D, 32, false>(a, ctas, st);
+    }
+}
+
+// What every entry point asks of the shape.
+static int check_shape(int B, int T_q, int H_q, int H_kv, int d, int window, int sinks) {
+    if (B < 0 || T_q <= 0 || H_q <= 0 || H_kv <= 0 || window < 0 || sinks < 0) return BDFP4_ERR_ARG;
+    if (H_q % H_kv) return BDFP4_ERR_SHAPE;
+    if (d != 64 && d != 128) return BDFP4_ERR_UNSUPPORTED;
+    // stacked rows, and grids of at most 2^31 - 1 blocks
+    if ((int64_t)T_q * (H_q / H_kv) > (1 << 24) || (int64_t)B * T_q * H_q > INT_MAX) return BDFP4_ERR_UNSUPPORTED;
+    return BDFP4_OK;
+}
+
+struct Shape {
+    int rows, groups, max_splits;
+};
+
+static Shape shape_of(int T_q, int H_q, int H_kv, int max_pages, int window, int sinks, int chunk) {
+    Shape s;
+    const int G = H_q / H_kv;
+    s.rows = rows_for(G, T_q);
+    s.groups = (int)(((int64_t)G * T_q + s.rows - 1) / s.rows);
+    const int64_t tiles = most_tiles((int64_t)max_pages * kPageSlots, T_q, G, s.rows, window, sinks);
+    s.max_splits = (int)std::max<int64_t>(1, (tiles + chunk - 1) / chunk);
+    return s;
+}
+
+// Tiles per split: CTAs of c tiles run in ceil(CTAs / slots) waves of c + 4 tile times (set-up, partial
+// write), and more than one split adds the merge's launch.  tiles_of(b): the tiles a row group
+// of sequence b sees at most.
+template <class TilesOf>
+static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int ctas) {
+    int64_t most = 1;
+    for (int b = 0; b < B; ++b) most = std::max<int64_t>(most, tiles_of(b));
+    const int64_t slots = (int64_t)std::max(1, sms) * ctas;
+    int64_t best_cost = -1;
+    int best = 1;
+    for (int64_t c = 1; c <= std::min<int64_t>(most, 128); ++c) {
+        int64_t n = 0;
+        for (int b = 0; b < B; ++b) n += (tiles_of(b) + c - 1) / c;
+        const int64_t cost = (n * items + slots - 1) / slots * (c + 4) + (c < most ? 4 : 0);
+        if (best_cost < 0 || cost <= best_cost) {
+            best_cost = cost;
+            best = (int)c;
+        }
+    }
+    return best;
+}
+
+}  // namespace fp8
+}  // namespace bdfp4
+
+using namespace bdfp4;
+using namespace bdfp4::fp8;
+
+extern "C" int bdfp8_decode_plan(const int32_t* host_seq_lens, int B, int T_q, int H_q, int H_kv, int d, int window,
+                                 int sinks, int num_sms) {
+    const int rc = check_shape(B, T_q, H_q, H_kv, d, window, sinks);
+    if (rc != BDFP4_OK) return rc;
+    if (num_sms <= 0 || (B > 0 && !host_seq_lens)) return BDFP4_ERR_ARG;
+    const Shape s = shape_of(T_q, H_q, H_kv, 1, window, sinks, 1);
+    return plan(
+        B,
+        [&](int b) { return most_tiles(std::max(0, host_seq_lens[b]), T_q, H_q / H_kv, s.rows, window, sinks); },
+        (int64_t)H_kv * s.groups, num_sms, ctas_per_sm(s.rows));
+}
+
+static size_t partial_bytes(int64_t rows, int max_splits, int d) {
+    const size_t o = (size_t)rows * max_splits * d * sizeof(float);
+    return (o + 255) / 256 * 256;
+}
+
+extern "C" size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, int d, int max_pages_per_seq,
+                                              int window, int sinks, int chunk_tiles) {
+    if (check_shape(B, T_q, H_q, H_kv, d, window, sinks) != BDFP4_OK || max_pages_per_seq <= 0 || chunk_tiles <= 0)
+        return 0;
+    const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, window, sinks, chunk_tiles);
+    if (s.max_splits <= 1) return 0;
+    const int64_t rows = (int64_t)B * T_q * H_q;
+    return partial_bytes(rows, s.max_splits, d) + (size_t)rows * s.max_splits * 2 * sizeof(float);
+}
+
+extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pages, const float* kv_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv,
+                            int d, int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, int window, int sinks,
+                            float sm_scale, int chunk_tiles, void* workspace, size_t workspace_bytes, void* out,
+                            int32_t* dev_status, void* stream) {
+    int rc = check_shape(B, T_q, H_q, H_kv, d, window, sinks);
+    if (rc != BDFP4_OK) return rc;
+    if (max_pages_per_seq <= 0 || num_pages < 0 || (fmt != BDFP8_E4M3 && fmt != BDFP8_E5M2)) return BDFP4_ERR_ARG;
+    // token indexes are 32-bit, with room for a window beyond them
+    if (max_pages_per_seq > (1 << 24) || num_pages > INT_MAX) return BDFP4_ERR_UNSUPPORTED;
+    if (B == 0) return BDFP4_OK;
+    if (!q || !k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !out) return BDFP4_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 128) || !aligned(v_pages, 128) ||
+        !aligned(kv_scales, 128) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        return BDFP4_ERR_ALIGN;
+    Args a{};
+    a.G = H_q / H_kv;
+    a.window = std::min(window, max_pages_per_seq * kPageSlots);
+    a.sinks = window > 0 ? std::min(sinks, max_pages_per_seq * kPageSlots) : 0;
+    if (chunk_tiles <= 0) {
+        int dev = 0, sms = 148;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return BDFP4_ERR_CUDA;
+        const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, a.window, a.sinks, 1);
+        const int64_t tiles = s.max_splits;   // at one tile per split
+        chunk_tiles = plan(1, [&](int) { return tiles; }, (int64_t)B * H_kv * s.groups, sms, ctas_per_sm(s.rows));
+    }
+    const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, a.window, a.sinks, chunk_tiles);
+    a.groups = s.groups;
+    a.max_splits = s.max_splits;
+    const int64_t ctas = (int64_t)B * H_kv * s.groups * s.max_splits;
+    if (ctas > INT_MAX) return BDFP4_ERR_UNSUPPORTED;
+    if (s.max_splits > 1) {
+        const int64_t rows = (int64_t)B * T_q * H_q;
+        const size_t o = partial_bytes(rows, s.max_splits, d);
+        if (!workspace || workspace_bytes < o + (size_t)rows * s.max_splits * 2 * sizeof(float))
+            return BDFP4_ERR_WORKSPACE;
+        if (!aligned(workspace, 128)) return BDFP4_ERR_ALIGN;
+        a.ws_o = (float*)workspace;
+        a.ws_ml = (float*)((char*)workspace + o);
+    }
+    a.q = (const __nv_bfloat16*)q;
+    a.k_pages = (const uint8_t*)k_pages;
+    a.v_pages = (const uint8_t*)v_pages;
+    a.kv_scales = kv_scales;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.out = (__nv_bfloat16*)out;
+    a.dev_status = dev_status;
+    a.B = B;
+    a.T_q = T_q;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.chunk_tiles = chunk_tiles;
+    a.sm_scale = sm_scale;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (fmt == BDFP8_E4M3)
+        return d == 128 ? dispatch<BDFP8_E4M3, 128>(a, s.rows, ctas, st) : dispatch<BDFP8_E4M3, 64>(a, s.rows, ctas, st);
+    return d == 128 ? dispatch<BDFP8_E5M2, 128>(a, s.rows, ctas, st) : dispatch<BDFP8_E5M2, 64>(a, s.rows, ctas, st);
+}
