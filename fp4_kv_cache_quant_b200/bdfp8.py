@@ -1,8 +1,9 @@
-"""Thin ctypes binding of the 8-bit paged cache (include/bdfp8.h).
+"""Thin binding of the 8-bit paged cache (include/bdfp8.h).
 
-Argument checks and marshalling only: the work runs in libbdfp4.so's CUDA
-kernels, on the current stream of the tensors' device.  The library and its
-errors are those of the ``bdfp4`` module.
+Argument checks and marshalling only (those of the append and the decode in an
+extension module, csrc/py_bdfp8.cpp, where a call costs microseconds less): the
+work runs in libbdfp4.so's CUDA kernels, on the current stream of the tensors'
+device.  The library and its errors are those of the ``bdfp4`` module.
 """
 from __future__ import annotations
 
@@ -24,10 +25,12 @@ DEV_BAD_POSITION = 16
 ENTRY_POINTS = ("bdfp8_append", "bdfp8_decode_plan", "bdfp8_decode_workspace_size", "bdfp8_decode")
 
 _lib = None
+_py = None
 
 
 def load() -> ctypes.CDLL:
-    global _lib
+    """Load libbdfp4.so and the extension module beside it (raises if they have not been built)."""
+    global _lib, _py
     if _lib is None:
         L = bdfp4.load()
         i, i64, p, f, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
@@ -40,41 +43,17 @@ def load() -> ctypes.CDLL:
         L.bdfp8_decode_workspace_size.restype = sz
         L.bdfp8_decode.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i64, i, i, i, f, i, p, sz, p, p, p]
         L.bdfp8_decode.restype = i
-        _lib = L
+        from . import _bdfp8_py
+        _bdfp8_py.set_error(BDFP4Error)
+        _lib, _py = L, _bdfp8_py
     return _lib
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise BDFP4Error(what)
-
-
-def _like(t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape, what: str) -> int:
-    """Data pointer of a contiguous tensor of this device, type and shape."""
-    if t.device != dev or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise BDFP4Error(f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-    return t.data_ptr()
-
-
-def _status(t: torch.Tensor | None, dev: torch.device):
-    if t is None:
-        return None
-    _need(t.device == dev and t.dtype == torch.int32 and t.numel() == 1, "dev_status: want one int32 on " + str(dev))
-    return t.data_ptr()
-
-
-def _call(fn, dev: torch.device, stream, what: str, *args):
-    """fn(*args, stream) with the tensors' device current, on `stream` or that device's current stream."""
-    if dev.type != "cuda":
-        raise BDFP4Error(f"{what}: tensors must be on a CUDA device, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
-    if rc != 0:
-        bdfp4._check(rc, what)
+def _calls():
+    """The extension module with the calls of a serving loop."""
+    if _py is None:
+        load()
+    return _py
 
 
 @dataclass
@@ -97,11 +76,6 @@ class FP8Cache:
     def nbytes(self) -> int:
         return self.k_pages.numel() + self.v_pages.numel() + 4 * self.kv_scales.numel()
 
-    def _ptrs(self, dev: torch.device):
-        n = (self.num_pages, self.H_kv, PAGE_SLOTS * self.d)
-        return (_like(self.k_pages, dev, torch.uint8, n, "k_pages"), _like(self.v_pages, dev, torch.uint8, n, "v_pages"),
-                _like(self.kv_scales, dev, torch.float32, (self.num_pages, self.H_kv, 2, 4), "kv_scales"))
-
 
 @dataclass
 class OpenBlocks:
@@ -115,15 +89,6 @@ class OpenBlocks:
         return OpenBlocks(mk(torch.float32), mk(torch.bfloat16))
 
 
-def _rows(t: torch.Tensor, dev, T, H, d, what: str):
-    """(pointer, token stride) of bf16 rows [T, H, d] with contiguous heads."""
-    if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or \
-            t.shape[2] != d or (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
-        raise BDFP4Error(f"{what}: want bf16 [{T}, {H}, {d}] on {dev} with contiguous heads, got {t.dtype} "
-                         f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * d)
-
-
 def bdfp8_append(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, seq_lens: torch.Tensor,
                  block_table: torch.Tensor, cos_sin: torch.Tensor | None, cache: FP8Cache, open_blocks: OpenBlocks,
                  q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
@@ -133,33 +98,14 @@ def bdfp8_append(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, seq_
     cu_tokens[b + 1] - 1 each; seq_lens counts them), rotating keys and, into q_out,
     queries q [T, H_q, d] by cos_sin [max_pos, rot_dim] (None: no rotation);
     interleaved pairs adjacent elements (bdfp8_append in bdfp8.h).  Returns q_out."""
-    dev, T, H, d = k.device, k.shape[0], cache.H_kv, cache.d
-    B, max_pages = block_table.shape
-    kp, ks = _rows(k, dev, T, H, d, "k")
-    vp, vs = _rows(v, dev, T, H, d, "v")
-    H_q, qp, qs, op = H, None, 0, None
-    if q is not None:
-        H_q = q.shape[1]
-        qp, qs = _rows(q, dev, T, H_q, d, "q")
-        if q_out is None:
-            q_out = torch.empty((T, H_q, d), dtype=torch.bfloat16, device=dev)
-        op = _like(q_out, dev, torch.bfloat16, (T, H_q, d), "q_out")
-    else:
-        _need(q_out is None, "q_out without q")
-    rot, max_pos, cs = 0, 0, None
-    if cos_sin is not None:
-        _need(cos_sin.dim() == 2, "cos_sin: want [max_pos, rot_dim]")
-        max_pos, rot = cos_sin.shape
-        cs = _like(cos_sin, dev, torch.float32, (max_pos, rot), "cos_sin")
-    pages = cache._ptrs(dev)
-    _call(load().bdfp8_append, dev, stream, "bdfp8_append", kp, ks, vp, vs, qp, qs, op,
-          _like(cu_tokens, dev, torch.int32, (B + 1,), "cu_tokens"), _like(seq_lens, dev, torch.int32, (B,), "seq_lens"),
-          None if positions is None else _like(positions, dev, torch.int32, (T,), "positions"), cs, rot, max_pos,
-          ROTATE_ADJACENT if interleaved else ROTATE_HALVES,
-          _like(open_blocks.k_open, dev, torch.float32, (B, BLOCK_TOKENS, H, d), "k_open"),
-          _like(open_blocks.v_open, dev, torch.bfloat16, (B, BLOCK_TOKENS, H, d), "v_open"),
-          _like(block_table, dev, torch.int32, (B, max_pages), "block_table"), B, T, H_q, H, d, max_pages,
-          cache.num_pages, cache.fmt, pages[0], pages[1], pages[2], _status(dev_status, dev))
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    rc = (_py or _calls()).append(
+        k, v, cu_tokens, seq_lens, block_table, cos_sin, cache.k_pages, cache.v_pages, cache.kv_scales, cache.num_pages,
+        cache.H_kv, cache.d, cache.fmt, open_blocks.k_open, open_blocks.v_open, q, q_out, positions,
+        ROTATE_ADJACENT if interleaved else ROTATE_HALVES, dev_status, stream and stream.cuda_stream)
+    if rc:
+        bdfp4._check(rc, "bdfp8_append")
     return q_out
 
 
@@ -192,18 +138,9 @@ def bdfp8_decode(q: torch.Tensor, cache: FP8Cache, block_table: torch.Tensor, se
     """Causal attention of each sequence's T_q newest tokens, q [B, T_q, H_q, d], over
     the 8-bit cache into out; window > 0 limits each to its window newest tokens
     and the first `sinks` (bdfp8_decode in bdfp8.h)."""
-    dev = q.device
-    B, T_q, H_q, d = q.shape
-    max_pages = block_table.shape[1]
-    _need(d == cache.d, f"q: head dim {d}, the cache has {cache.d}")
-    pages = cache._ptrs(dev)
-    wp, wb = None, 0
-    if workspace is not None:
-        _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: want contiguous memory on {dev}")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(load().bdfp8_decode, dev, stream, "bdfp8_decode", _like(q, dev, torch.bfloat16, q.shape, "q"), pages[0], pages[1],
-          pages[2], _like(block_table, dev, torch.int32, (B, max_pages), "block_table"),
-          _like(seq_lens, dev, torch.int32, (B,), "seq_lens"), B, T_q, H_q, cache.H_kv, d, max_pages, cache.num_pages,
-          cache.fmt, window, sinks, sm_scale, chunk_tiles, wp, wb, _like(out, dev, torch.bfloat16, q.shape, "out"),
-          _status(dev_status, dev))
+    rc = (_py or _calls()).decode(
+        q, cache.k_pages, cache.v_pages, cache.kv_scales, cache.num_pages, cache.H_kv, cache.d, cache.fmt, block_table,
+        seq_lens, sm_scale, chunk_tiles, workspace, out, window, sinks, dev_status, stream and stream.cuda_stream)
+    if rc:
+        bdfp4._check(rc, "bdfp8_decode")
     return out

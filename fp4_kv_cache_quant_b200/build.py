@@ -2,7 +2,9 @@
 
 Each translation unit compiles to an object of its own, in parallel (one nvcc
 process per .cu file, under _build/ beside this file), and nvcc links them
-into the shared library."""
+into the shared library.  The Python side of the 8-bit cache's calls
+(csrc/py_bdfp8.cpp, an extension module against this interpreter and torch)
+compiles beside them and links to that library."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -10,10 +12,13 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbdfp4.so")
+PY_SRC = os.path.join(CSRC, "py_bdfp8.cpp")
+PY_LIB = os.path.join(HERE, "_bdfp8_py.so")
 OBJ = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -32,10 +37,34 @@ def _headers() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PY_LIB):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in sources() + _headers())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
+    return any(os.path.getmtime(p) > t for p in [*sources(), PY_SRC, *_headers()])
+
+
+def _compile_py(verbose: bool) -> tuple[str, str]:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(OBJ, "py_bdfp8.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", "-o", obj, PY_SRC,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in (os.path.join(root, "include"), sysconfig.get_paths()["include"],
+                                os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"))]]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on py_bdfp8.cpp:\n{r.stdout}{r.stderr}")
+    return obj, r.stdout + r.stderr
+
+
+def _link_py(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    subprocess.run(["g++", "-shared", "-o", PY_LIB + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-ltorch_python",
+                    "-ltorch_cpu", "-lc10_cuda", "-lc10"], check=True)
+    os.replace(PY_LIB + ".tmp", PY_LIB)
 
 
 def _compile(src: str, extra: list[str], verbose: bool) -> tuple[str, str]:
@@ -50,21 +79,25 @@ def _compile(src: str, extra: list[str], verbose: bool) -> tuple[str, str]:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:
-    """Compile csrc/*.cu into libbdfp4.so (or `out`) unless it is up to date."""
+    """Compile csrc/*.cu into libbdfp4.so (or `out`; then without the extension module) unless it is up to date."""
     target = out or LIB
     if not force and out is None and not _stale():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+        py = ex.submit(_compile_py, verbose) if out is None else None
         results = list(ex.map(lambda s: _compile(s, extra or [], verbose), srcs))
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log, end="", flush=True)
-    cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", target + ".tmp", *[o for o, _ in results]]
+    soname = ["-Xlinker", "-soname=" + os.path.basename(LIB)]   # what the extension module looks for beside it
+    cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *soname, "-o", target + ".tmp", *[o for o, _ in results]]
     subprocess.run(cmd, check=True)
     os.replace(target + ".tmp", target)
+    if py is not None:
+        _link_py(py.result()[0])
     return target
 
 

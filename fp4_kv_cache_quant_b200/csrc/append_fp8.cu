@@ -2,8 +2,8 @@
 // with the position rotation of keys and queries on the way.
 //
 // One CTA per (block of 16 tokens that the call touches, KV head): D threads for
-// the keys (a row's 16 elements each), D for the values (a channel each), and all
-// of them for the rotation of the group's queries.  The work is moving bytes
+// the keys (16 elements of a row each), D for the values (two channels of eight
+// rows each), and all of them for the rotation of the group's queries.  The work is moving bytes
 // (2 B in, 1 B out per key and value element, 2 + 2 per query element); a block's
 // scale needs its maximum first, so its elements wait in registers.
 //
@@ -62,39 +62,60 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* x) {
     }
 }
 
-__device__ __forceinline__ void load4(const float* p, float* x) {
-    *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(p));
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    uint4 o;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return o;
 }
 
-// Elements e0 .. e0 + 7 of a row rotated by `cs` (rot / 2 cosines, then as many sines; null = not rotated).
+__device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4* v = reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(x) = v[0];
+    *reinterpret_cast<float4*>(x + 4) = v[1];
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    float4* v = reinterpret_cast<float4*>(p);
+    v[0] = *reinterpret_cast<const float4*>(x);
+    v[1] = *reinterpret_cast<const float4*>(x + 4);
+}
+
+// A row is handled in units of 16 elements, 8 from ea and 8 from eb, that hold both sides of
+// their rotated pairs and share 8 cosines and sines: with halves paired, elements 8 u.. and 8 u + rot / 2..;
+// else, and behind rot, 16 u.. and 16 u + 8...
+struct Unit {
+    int u, ea, eb;
+    __device__ __forceinline__ Unit(int u_, int rot, int adjacent) : u(u_) {
+        const bool halves = !adjacent && 16 * u < rot;
+        ea = halves ? 8 * u : 16 * u;
+        eb = halves ? 8 * u + (rot >> 1) : 16 * u + 8;
+    }
+};
+
+// The unit's elements a[8], b[8] rotated by `cs` (rot / 2 cosines, then as many sines; null = not rotated).
 template <bool EXACT>
-__device__ __forceinline__ void rotated8(const __nv_bfloat16* row, int e0, const float* cs, int rot, bool adjacent,
-                                         float* x) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(row + e0)), x);
-    if (!cs || e0 >= rot) return;
-    auto comb = [](float a, float c, float b, float s) { return EXACT ? turn(a, c, b, s) : fmaf(a, c, -(b * s)); };
-    const int half = rot >> 1;
-    if (adjacent) {
-        float c[4], s[4];
-        load4(cs + (e0 >> 1), c);
-        load4(cs + half + (e0 >> 1), s);
+__device__ __forceinline__ void rotate(float* a, float* b, const Unit& un, const float* cs, int rot, int adjacent) {
+    if (!cs || 16 * un.u >= rot) return;
+    auto comb = [](float x, float c, float y, float s) { return EXACT ? turn(x, c, y, s) : fmaf(x, c, -(y * s)); };
+    float c[8], s[8];
+    load8(cs + 8 * un.u, c);
+    load8(cs + (rot >> 1) + 8 * un.u, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = comb(a, c[i], b, s[i]);
-            x[2 * i + 1] = comb(b, c[i], a, -s[i]);
+    for (int i = 0; i < 8; ++i) {
+        if (!adjacent) {
+            const float x = a[i], y = b[i];
+            a[i] = comb(x, c[i], y, s[i]);
+            b[i] = comb(y, c[i], x, -s[i]);
+        } else {
+            float* const p = (i < 4 ? a : b) + 2 * (i & 3);
+            const float x = p[0], y = p[1];
+            p[0] = comb(x, c[i], y, s[i]);
+            p[1] = comb(y, c[i], x, -s[i]);
         }
-    } else {
-        const bool lower = e0 < half;
-        const int f = lower ? e0 : e0 - half;
-        float y[8], c[8], s[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(row + (lower ? e0 + half : e0 - half))), y);
-        load4(cs + f, c);
-        load4(cs + f + 4, c + 4);
-        load4(cs + half + f, s);
-        load4(cs + half + f + 4, s + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = comb(x[i], c[i], y[i], lower ? s[i] : -s[i]);
     }
 }
 
@@ -107,8 +128,9 @@ __device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const AppendArgs a) {
     constexpr int WK = D / 32;             // warps of the keys, and of the values
+    constexpr int UNITS = D / 16;          // units of a row
     constexpr int PAGE = kPageSlots * D;
     __shared__ uint32_t red[2][WK];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -121,9 +143,10 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
                 set_status(a.dev_status, BDFP4_DEV_BAD_SEQLEN);
         }
 
-    // the last b with cu[b] / 16 + 2 b <= item
+    // The last b with cu[b] / 16 + 2 b <= item: down to 31 candidates, whose entries and lengths the lanes
+    // then hold (one round of loads for up to 31 sequences).
     int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
+    while (hi - lo > 31) {
         const int step = (hi - lo + 31) >> 5;
         const int at = lo + lane * step;
         const bool le = at < hi && (lane == 0 || (__ldg(a.cu + at) >> 4) + 2 * at <= item);
@@ -131,8 +154,13 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
         lo += k * step;
         hi = min(hi, lo + step);
     }
-    const int b = lo;
-    const int c0 = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - c0, end = __ldg(a.seq_lens + b);
+    const int mine_b = lo + lane;
+    const int cu_l = mine_b <= hi ? __ldg(a.cu + mine_b) : 0;
+    const int len_l = mine_b < hi ? __ldg(a.seq_lens + mine_b) : 0;
+    const int at_l = __popc(__ballot_sync(0xffffffffu, mine_b < hi && (lane == 0 || (cu_l >> 4) + 2 * mine_b <= item))) - 1;
+    const int b = lo + at_l;
+    const int c0 = __shfl_sync(0xffffffffu, cu_l, at_l), n = __shfl_sync(0xffffffffu, cu_l, at_l + 1) - c0;
+    const int end = __shfl_sync(0xffffffffu, len_l, at_l);
     if (n <= 0 || c0 < 0 || c0 > a.T - n || end < n || end > a.max_pages * kPageSlots) return;
     const int start = end - n;
     const int blk0 = start / kBlockTokens, last = (end - 1) / kBlockTokens;
@@ -150,6 +178,39 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
         return a.cos_sin + (int64_t)pos * a.rot;
     };
 
+    // Queries of the group: one unit per thread and step.  The first two steps' loads go out before the
+    // keys and values are worked on.
+    const int q0 = max(mine * kBlockTokens, start), per = a.G * UNITS;
+    const int nq = a.q ? (min((mine + 1) * kBlockTokens, end) - q0) * per : 0;
+    auto q_row = [&](int x, int& t, int& h) {
+        const int i = x / per;
+        t = c0 + q0 + i - start;
+        h = hk * a.G + (x - i * per) / UNITS;
+    };
+    const Unit qu(tid % UNITS, a.rot, a.adjacent);   // alike in every step: 2 D is a multiple of UNITS
+    auto q_load = [&](int x, uint4* w) {
+        int t, h;
+        q_row(x, t, h);
+        const __nv_bfloat16* row = a.q + t * a.q_stride + h * D;
+        w[0] = __ldg(reinterpret_cast<const uint4*>(row + qu.ea));
+        w[1] = __ldg(reinterpret_cast<const uint4*>(row + qu.eb));
+    };
+    auto q_store = [&](int x, const uint4* w) {
+        int t, h;
+        q_row(x, t, h);
+        float f[8], g[8];
+        unpack8(w[0], f);
+        unpack8(w[1], g);
+        rotate<false>(f, g, qu, angles(t, start + t - c0), a.rot, a.adjacent);
+        __nv_bfloat16* row = a.q_out + ((int64_t)t * a.H_q + h) * D;
+        *reinterpret_cast<uint4*>(row + qu.ea) = pack8(f);
+        *reinterpret_cast<uint4*>(row + qu.eb) = pack8(g);
+    };
+    uint4 qw[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (tid + i * 2 * D < nq) q_load(tid + i * 2 * D, qw[i]);
+
     // Blocks of this CTA: its own; and, where the sequence's first block has open rows and is not its last,
     // the first block's CTA does the last one too, after it has read the open rows that the last one replaces.
     const bool reads_open = start % kBlockTokens != 0;
@@ -163,47 +224,52 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
             const int64_t ph = (int64_t)page * a.H_kv + hk;
             const int slot0 = i0 % kPageSlots;
             const bool is_v = tid >= D;
+            // keys: row tid / UNITS, one unit; values: channels 2 c and 2 c + 1 of eight rows
+            const int kr = tid / UNITS;
+            const Unit ku(tid % UNITS, a.rot, a.adjacent);
+            const int vc = tid % (D / 2) * 2, vr = (tid - D) / (D / 2) * 8;
             float x[16];
-            uint32_t mx = 0;
             if (!is_v) {
-                // keys: row tid / (D / 16), elements 16 c .. 16 c + 15
-                const int r = tid / (D / 16), c = tid % (D / 16), i = i0 + r;
-                const int64_t open = (((int64_t)b * kBlockTokens + r) * a.H_kv + hk) * D + 16 * c;
+                const int i = i0 + kr;
+                float* const open = a.k_open + (((int64_t)b * kBlockTokens + kr) * a.H_kv + hk) * D;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = 0.0f;
                 if (i < start) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(a.k_open + open + e);
+                    load8(open + ku.ea, x);
+                    load8(open + ku.eb, x + 8);
                 } else if (i < end) {
                     const int t = c0 + i - start;
                     const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
-                    const float* cs = angles(t, i);
-                    rotated8<true>(row, 16 * c, cs, a.rot, a.adjacent, x);
-                    rotated8<true>(row, 16 * c + 8, cs, a.rot, a.adjacent, x + 8);
+                    const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + ku.ea));
+                    const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + ku.eb));
+                    unpack8(w0, x);
+                    unpack8(w1, x + 8);
+                    rotate<true>(x, x + 8, ku, angles(t, i), a.rot, a.adjacent);
                     if (blk == last) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(a.k_open + open + e) = *reinterpret_cast<const float4*>(x + e);
+                        store8(open + ku.ea, x);
+                        store8(open + ku.eb, x + 8);
                     }
                 }
             } else {
-                // values: channel tid - D, one register per token
-                const int ch = tid - D;
+                uint32_t w[8];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int i = i0 + r;
-                    __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + r) * a.H_kv + hk) * D + ch;
-                    if (i < start) {
-                        x[r] = __bfloat162float(*open);
-                    } else if (i < end) {
-                        const __nv_bfloat16 w = a.v[(int64_t)(c0 + i - start) * a.v_stride + hk * D + ch];
-                        x[r] = __bfloat162float(w);
-                        if (blk == last) *open = w;
-                    } else {
-                        x[r] = 0.0f;
-                    }
+                for (int r = 0; r < 8; ++r) {
+                    const int i = i0 + vr + r;
+                    __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + vr + r) * a.H_kv + hk) * D + vc;
+                    const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i - start) * a.v_stride + hk * D + vc;
+                    w[r] = i < end ? *reinterpret_cast<const uint32_t*>(i < start ? open : row) : 0u;
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int i = i0 + vr + r;
+                    if (blk == last && i >= start && i < end)
+                        *reinterpret_cast<uint32_t*>(a.v_open + (((int64_t)b * kBlockTokens + vr + r) * a.H_kv + hk) * D + vc) = w[r];
+                    x[r] = __uint_as_float(w[r] << 16);
+                    x[8 + r] = __uint_as_float(w[r] & 0xffff0000u);
                 }
             }
             // as bits, a NaN is above an infinity and that above every number
+            uint32_t mx = 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
             mx = __reduce_max_sync(0xffffffffu, mx);
@@ -214,20 +280,24 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
             for (int w = 1; w < WK; ++w) mx = max(mx, red[is_v][w]);
             const int e = scale_exp<FMT>(mx);
             const float inv = pow2i(-e);
-            uint32_t w[4];
+            uint2 w[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = f8x2<FMT>(x[4 * i] * inv, x[4 * i + 1] * inv) | (f8x2<FMT>(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+            for (int i = 0; i < 2; ++i) {
+                const float* y = x + 8 * i;
+                w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
+                w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
+            }
             if (page_ok) {
-                uint8_t* dst;
                 if (!is_v) {
-                    const int s = slot0 + tid / (D / 16);
-                    dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (tid % (D / 16)) * 128 + (s & 7) * 16;
+                    const int s = slot0 + kr;
+                    uint8_t* const dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (s & 7) * 16;
+                    *reinterpret_cast<uint2*>(dst + (ku.ea >> 4) * 128 + (ku.ea & 15)) = w[0];
+                    *reinterpret_cast<uint2*>(dst + (ku.eb >> 4) * 128 + (ku.eb & 15)) = w[1];
                 } else {
-                    const int ch = tid - D;
-                    dst = a.v_pages + ph * PAGE + (ch >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (ch & 7) * 16;
+                    uint8_t* const dst = a.v_pages + ph * PAGE + (vc >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (vc & 7) * 16 + vr;
+                    *reinterpret_cast<uint2*>(dst) = w[0];
+                    *reinterpret_cast<uint2*>(dst + 16) = w[1];
                 }
-                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
                 if (tid == 0 || tid == D)
                     a.kv_scales[ph * kScalePage + (is_v ? kBlocksPerPage : 0) + slot0 / kBlockTokens] =
                         mx >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : pow2i(e);
@@ -238,24 +308,16 @@ __global__ void __launch_bounds__(2 * D) append_fp8_kernel(const AppendArgs a) {
         __syncthreads();   // the open rows of the first block are read, its maxima too
     }
 
-    // queries of the group: 8 elements per thread and step
-    if (a.q) {
-        const int i0 = max(mine * kBlockTokens, start), i1 = min((mine + 1) * kBlockTokens, end);
-        const int per = a.G * (D / 8);
-        for (int u = tid; u < (i1 - i0) * per; u += 2 * D) {
-            const int i = i0 + u / per, w = u % per, t = c0 + i - start;
-            const int h = hk * a.G + w / (D / 8), e0 = w % (D / 8) * 8;
-            float x[8];
-            rotated8<false>(a.q + t * a.q_stride + h * D, e0, angles(t, i), a.rot, a.adjacent, x);
-            uint4 o;
-            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-                ow[e] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            *reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * a.H_q + h) * D + e0) = o;
-        }
+    for (int i = 0; i < 2; ++i)
+        if (tid + i * 2 * D < nq) q_store(tid + i * 2 * D, qw[i]);
+    for (int x = tid + 4 * D; x < nq; x += 4 * D) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (x + i * 2 * D < nq) q_load(x + i * 2 * D, qw[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (x + i * 2 * D < nq) q_store(x + i * 2 * D, qw[i]);
     }
 }
 
