@@ -87,7 +87,7 @@ struct Cfg {
     static constexpr int NQ = 2 * ROWS < 16 ? 16 : 2 * ROWS;      // N of QK: q1 and q2 columns
     static constexpr int NP = (3 * ROWS + 15) / 16 * 16;          // N of PV: three probability terms
     static constexpr int KS = D / 32;                             // MMA K steps of QK
-    static constexpr int NSG = 2;                                 // softmax groups of four warps
+    static constexpr int NSG = ROWS >= 16 ? 4 : 2;                // softmax groups of four warps
     static constexpr int HG = ROWS / NSG;                         // rows per group
     static constexpr int HB = HG < 8 ? HG : 8;                    // rows handled at once
     static constexpr int NSW = 4 * NSG;
@@ -97,9 +97,14 @@ struct Cfg {
     static constexpr int CTAS = ROWS <= 8 ? 3 : (ROWS == 16 ? 2 : 1);
     static constexpr int NSK = CTAS == 3 ? 2 : 3, NSV = CTAS == 1 ? 3 : 2;
     static constexpr int NSC = NSK <= 2 ? 4 : 8;                  // scale slots (at least NSK + 2, see the producer)
+    // P: [token/16][row][16 tokens] with chunks an odd multiple of 64 bytes apart, so that a warp's byte
+    // stores (32 tokens of a row, two chunks) meet no bank twice.  MMA rows behind 3 ROWS read on into
+    // what follows; their columns are not used.
+    static constexpr int P_CHUNK = (3 * ROWS * 16) % 128 == 64 ? 3 * ROWS * 16 : 3 * ROWS * 16 + 64;
+    static_assert(P_CHUNK % 128 == 64, "bank spread");
     static constexpr int PAGE = kPageSlots * D;
     static constexpr int TILE = 2 * PAGE;
-    static constexpr int P_BUF = NP * kTileTokens;                // [row/8][token/16][row%8][16]
+    static constexpr int P_BUF = 8 * P_CHUNK;
     static constexpr int SM_K = 0;
     static constexpr int SM_V = SM_K + NSK * TILE;
     // D = 64: the value MMA's M = 128 rows run 4 KB past a page, into the bytes that follow the
@@ -107,7 +112,7 @@ struct Cfg {
     static constexpr int SM_P = SM_V + NSV * TILE;
     static constexpr int SM_Q = SM_P + 2 * P_BUF;
     static constexpr int SM_SC = SM_Q + NQ * D;                                // [NSC][2 pages][8] scales
-    static constexpr int RED_Q = ROWS + 2;                                    // a quadrant's maxima: rows, scale of each group
+    static constexpr int RED_Q = ROWS + NSG;                                    // a quadrant's maxima: rows, scale of each group
     static constexpr int SM_RED = SM_SC + NSC * 2 * kScalePage * 4;           // [2][4][RED_Q]
     static constexpr int SM_VM = (SM_RED + 2 * 4 * RED_Q * 4 + 15) / 16 * 16;   // [2][NSG][4] masks of visible tokens
     static constexpr int SM_LSC = SM_VM + 2 * NSG * 16;                       // [ROWS] logit factors
@@ -116,7 +121,8 @@ struct Cfg {
     static constexpr int NBARS = 2 * NSK + 2 * NSV + 7;
     static constexpr int SM_MISC = SM_BARS + NBARS * 8;
     static constexpr int SMEM = SM_MISC + 16;
-    static_assert(2 * P_BUF >= 4096, "the value MMA's overrun at D = 64 stays inside the block's memory");
+    static_assert(2 * P_BUF + NQ * D >= 4096, "the value MMA's overrun at D = 64 stays inside the block's memory");
+    static_assert((NP - 3 * ROWS) * 16 <= NQ * D, "P's overrun too");
     static_assert(SMEM <= 233472 / CTAS - 1024, "shared memory");
     static_assert(NSC >= NSK + 2, "scale slots");
     static constexpr int T_S = 0;                                 // TMEM columns: S^T double buffer, O^T
@@ -337,12 +343,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 if (!(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit))) break;
                 tc::tc_fence_after();
                 const uint32_t vt = v_addr + s * C::TILE;
-                // V^T: 8-channel groups 512 bytes apart, 16-slot chunks 128 apart; P: 8-row groups 1 KB
+                // V^T: 8-channel groups 512 bytes apart, 16-slot chunks 128 apart; P: 8-row groups 128 bytes
                 // apart.  O^T accumulates over the split's tiles (the softmax warps rescale it).
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_f8(tbase + C::T_O, tc::smem_desc(vt + (ks >> 1) * C::PAGE + (ks & 1) * 256, 128, 512),
-                           tc::smem_desc(p_addr + buf * C::P_BUF + ks * 256, 128, 1024), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
+                           tc::smem_desc(p_addr + buf * C::P_BUF + ks * 2 * C::P_CHUNK, C::P_CHUNK, 128), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
                 tc::mma_commit(&o_full[buf]);
                 tc::mma_commit(&vempty[s]);
                 last_bar = &vempty[s];
@@ -424,7 +430,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         const int blk = 2 * (qd & 1) + (lane >> 4);            // its scale block in the page
         const int tok = 32 * qd + lane;
         const int chan = tok;                                  // O^T lane = value channel
-        uint8_t* const pslot = p_op + (tok >> 4) * 128 + (tok & 15);
+        uint8_t* const pslot = p_op + (tok >> 4) * C::P_CHUNK + 3 * gb * 16 + (tok & 15);
+        float lr[HG];
+#pragma unroll
+        for (int g = 0; g < HG; ++g) lr[g] = lsc[gb + g];
         const uint32_t t_o = tq + C::T_O + 3 * gb;             // a group's first, second and third terms
 
         for (int j = 0; j < n; ++j) {
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int g = 0; g < HB; ++g) {
-                    const float s = fmaf(__uint_as_float(s2[g]), 0.0625f, __uint_as_float(s1[g])) * ka * lsc[gb + g0 + g];
+                    const float s = fmaf(__uint_as_float(s2[g]), 0.0625f, __uint_as_float(s1[g])) * (ka * lr[g0 + g]);
                     const bool see = valid && (!MT || (g0 + g >= vis0 && g0 + g < vis1));
                     x[g0 + g] = see ? s : -INFINITY;
                 }
@@ -495,13 +504,17 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             // value scale in units of 2^(ev - 15); nothing of a token that no row sees goes in
             const float vy = valid ? va * pow2i(-en) * 32768.0f : 0.0f;
             uint8_t* const pb = pslot + buf * C::P_BUF;
+            if (rose) {
+#pragma unroll
+                for (int g = 0; g < HG; ++g) l_part[g] *= __shfl_sync(0xffffffffu, corr_l, g);
+            }
 #pragma unroll
             for (int g = 0; g < HG; g += 2) {
                 constexpr int H1 = HG > 1 ? 1 : 0;
                 const float p0 = tc::ex2_approx(x[g] - __shfl_sync(0xffffffffu, mz, g));
                 const float p1 = tc::ex2_approx(x[g + H1] - __shfl_sync(0xffffffffu, mz, g + H1));
-                l_part[g] = fmaf(l_part[g], __shfl_sync(0xffffffffu, corr_l, g), p0);
-                l_part[g + H1] = fmaf(l_part[g + H1], __shfl_sync(0xffffffffu, corr_l, g + H1), p1);
+                l_part[g] += p0;
+                l_part[g + H1] += p1;
                 // three E5M2 terms of p c: each leaves what it cannot hold (exact in fp16) to the next.
                 // An E5M2 code is the upper byte of the fp16 with its value.
                 __half2 y = __floats2half2_rn(p0 * vy, p1 * vy);
@@ -509,9 +522,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 for (int k = 0; k < 3; ++k) {
                     uint16_t c;
                     asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t*>(&y)));
-                    const int r = 3 * gb + k * HG + g;
-                    pb[(r >> 3) * 1024 + (r & 7) * 16] = (uint8_t)c;
-                    pb[((r + H1) >> 3) * 1024 + ((r + H1) & 7) * 16] = (uint8_t)(c >> 8);
+                    pb[(k * HG + g) * 16] = (uint8_t)c;
+                    pb[(k * HG + g + H1) * 16] = (uint8_t)(c >> 8);
                     if (k < 2) {
                         const uint32_t back = __byte_perm((uint32_t)c, 0u, 0x1404);
                         y = __hsub2(y, *reinterpret_cast<const __half2*>(&back));
