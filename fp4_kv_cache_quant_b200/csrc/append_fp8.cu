@@ -278,12 +278,16 @@ __global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const Append
             mx = red[is_v][0];
 #pragma unroll
             for (int w = 1; w < WK; ++w) mx = max(mx, red[is_v][w]);
+            // a block with an infinity or a NaN says so by its scale; its codes are 0, which no product spreads to
+            // rows that do not see the block
+            const bool finite = mx < 0x7f800000u;
             const int e = scale_exp<FMT>(mx);
             const float inv = pow2i(-e);
-            uint2 w[2];
+            uint2 w[2] = {};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float* y = x + 8 * i;
+                if (!finite) continue;
                 w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
                 w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
             }
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const Append
                 }
                 if (tid == 0 || tid == D)
                     a.kv_scales[ph * kScalePage + (is_v ? kBlocksPerPage : 0) + slot0 / kBlockTokens] =
-                        mx >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : pow2i(e);
+                        finite ? pow2i(e) : __uint_as_float(0x7fc00000u);
             }
         }
         if (!(chained && blk == blk0)) break;

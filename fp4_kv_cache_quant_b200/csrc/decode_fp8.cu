@@ -16,11 +16,11 @@
 // The terms are stacked as columns of one MMA (N = 2 rows of q, 3 rows of P), S^T =
 // K q^T with M = 128 tokens and O^T = V^T P^T with M = 128 channels.
 //
-// One CTA per (sequence, KV head, group of up to 32 stacked query rows, split):
-// eight softmax warps in two groups that each own half of the rows (thread = token,
-// then thread = channel), a producer warp (bulk copies into a key and a value ring;
-// keys run one tile ahead) and an MMA warp.  Query rows are the G T_q (token, head)
-// rows of the KV head.
+// One CTA per (sequence, KV head, split), for up to eight stacked query rows, the G
+// T_q (token, head) rows of the KV head (more take decode_fp8_wide.cu): eight softmax
+// warps in two groups that each own half of the rows (thread = token, then thread =
+// channel), a producer warp (bulk copies into a key and a value ring; keys run one
+// tile ahead) and an MMA warp.
 //
 // A row group's tiles are those of the first `sinks` tokens and those from its oldest
 // window token on, numbered one after another and cut into splits, so a window
@@ -29,74 +29,25 @@
 #include <algorithm>
 #include <climits>
 
-#include "decode_common.cuh"
-#include "fp8_device.cuh"
-#include "host_common.h"
+#include "decode_fp8.cuh"
 
 namespace bdfp4 {
 namespace fp8 {
-
-struct Args {
-    const __nv_bfloat16* q;
-    const uint8_t* k_pages;
-    const uint8_t* v_pages;
-    const float* kv_scales;
-    const int32_t* block_table;
-    const int32_t* seq_lens;
-    float* ws_o;    // [B T_q H_q][max_splits][d] unnormalised partial outputs
-    float* ws_ml;   // [B T_q H_q][max_splits][2] (m in log2 units, l)
-    __nv_bfloat16* out;
-    int32_t* dev_status;
-    int B, T_q, H_q, H_kv, G, max_pages, window, sinks, chunk_tiles, max_splits, groups;
-    int64_t num_pages;
-    float sm_scale;
-};
-
-// The tiles that rows r0 .. r1 of a KV head's stacked rows see (row r is query token r / G).
-struct Tiles {
-    int end;      // tokens from here on are seen by none of the rows
-    int lo;       // first token of the oldest window (0 without a window)
-    int front;    // tiles of the first tokens, before the window's tiles
-    int first;    // first tile of the window
-    int total;
-    __device__ __forceinline__ int tile(int v) const { return v < front ? v : first + v - front; }
-};
-
-__device__ __forceinline__ Tiles tiles_of(int N, int T_q, int G, int r0, int r1, int window, int sinks) {
-    Tiles t;
-    t.end = max(0, N - T_q + r1 / G + 1);
-    t.lo = window > 0 ? max(0, N - T_q + r0 / G - window + 1) : 0;
-    t.lo = min(t.lo, t.end);
-    const int last = (t.end + kTileTokens - 1) / kTileTokens;
-    t.first = t.lo / kTileTokens;
-    t.front = window > 0 ? min((min(sinks, t.end) + kTileTokens - 1) / kTileTokens, t.first) : 0;
-    t.total = t.front + last - t.first;
-    return t;
-}
-
-__device__ __forceinline__ int splits_of(const Tiles& t, int chunk) { return (t.total + chunk - 1) / chunk; }
-
-// A length out of range counts as an empty sequence.
-__device__ __forceinline__ int checked_len(const Args& a, int b) {
-    const int N = a.seq_lens[b];
-    return N < 0 || N > a.max_pages * kPageSlots ? 0 : N;
-}
 
 template <int FMT, int D, int ROWS, bool MT>
 struct Cfg {
     static constexpr int NQ = 2 * ROWS < 16 ? 16 : 2 * ROWS;      // N of QK: q1 and q2 columns
     static constexpr int NP = (3 * ROWS + 15) / 16 * 16;          // N of PV: three probability terms
     static constexpr int KS = D / 32;                             // MMA K steps of QK
-    static constexpr int NSG = ROWS >= 16 ? 4 : 2;                // softmax groups of four warps
+    static constexpr int NSG = ROWS == 16 ? 4 : 2;                // softmax groups of four warps
     static constexpr int HG = ROWS / NSG;                         // rows per group
-    static constexpr int HB = HG < 8 ? HG : 8;                    // rows handled at once
     static constexpr int NSW = 4 * NSG;
     static constexpr int PRODUCER = NSW, MMA_WARP = NSW + 1;
     static constexpr int THREADS = 32 * (NSW + 2);
     // Up to eight rows an SM holds three blocks of two 16 KB key and two value stages (192 KB in flight).
-    static constexpr int CTAS = ROWS <= 8 ? 3 : (ROWS == 16 ? 2 : 1);
-    static constexpr int NSK = CTAS == 3 ? 2 : 3, NSV = CTAS == 1 ? 3 : 2;
-    static constexpr int NSC = NSK <= 2 ? 4 : 8;                  // scale slots (at least NSK + 2, see the producer)
+    static constexpr int CTAS = ROWS == 16 ? 2 : 3;
+    static constexpr int NSK = ROWS == 16 ? 3 : 2, NSV = 2;
+    static constexpr int NSC = ROWS == 16 ? 8 : 4;                  // scale slots (at least NSK + 2, see the producer)
     // P: [token/16][row][16 tokens] with chunks an odd multiple of 64 bytes apart, so that a warp's byte
     // stores (32 tokens of a row, two chunks) meet no bank twice.  MMA rows behind 3 ROWS read on into
     // what follows; their columns are not used.
@@ -128,17 +79,16 @@ struct Cfg {
     static constexpr int T_S = 0;                                 // TMEM columns: S^T double buffer, O^T
     static constexpr int T_O = 2 * NQ;
     static constexpr int T_USED = T_O + NP;
-    static constexpr int T_ALLOC = T_USED <= 64 ? 64 : (T_USED <= 128 ? 128 : 256);
-    static_assert(T_USED <= 256 && T_ALLOC * CTAS <= 512, "tensor memory");
+    static constexpr int T_ALLOC = ROWS == 16 ? 128 : 64;
+    static_assert(T_USED <= T_ALLOC && T_ALLOC * CTAS <= 512, "tensor memory");
+    static_assert(ROWS == 4 || ROWS == 8 || ROWS == 16, "more rows take the wide kernel");
 };
-
-constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 
 template <int FMT, int D, int ROWS, bool MT>
 __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, ROWS, MT>::CTAS)
     decode_fp8_kernel(const Args a) {
     using C = Cfg<FMT, D, ROWS, MT>;
-    constexpr int HG = C::HG, HB = C::HB;
+    constexpr int HG = C::HG;
     // the split merge (a programmatic dependent) may be scheduled as CTAs of this grid retire
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -216,102 +166,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     const uint32_t tbase = *tmem_slot;
 
     if (warp == C::PRODUCER) {
-        // ------------------------------------------------------------ producer
-        // Step k issues the keys and scales of tile k and the values of tile k - 1, so keys run a
-        // tile ahead.  Lanes read the page ids of 32 tiles at once; one lane per copy issues.
-        // Scales go to slot k % NSC with the keys' byte count.  A key stage is refilled once its QK
-        // has completed, and the MMA lane issues QK of tile t only after p_ready of tile t - 2: when
-        // tile k's keys are issued, the softmax is done with the scales of tile k - NSK - 2, and
-        // with NSC >= NSK + 2 slot k % NSC is free.
-        bool ok = true;
-        int pv[2] = {-1, -1};
-        int k_last = -1, v_last = -1;
-        for (int j0 = 0; ok && j0 <= n; j0 += 32) {
-            int pg_l[2] = {-1, -1};
-            if (j0 + lane < n) {
-                const int tile = tl.tile(tile0 + j0 + lane);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const int pi = tile * 2 + p, t0 = pi * kPageSlots;
-                    // pages that no row sees are not looked up
-                    if (t0 < tl.end && (t0 + kPageSlots > tl.lo || t0 < a.sinks)) {
-                        const int v = a.block_table[(int64_t)b * a.max_pages + pi];
-                        if (v >= 0 && v < a.num_pages) pg_l[p] = v;
-                        else set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
-                    }
-                }
-            }
-            const int kmax = min(32, n + 1 - j0);
-            for (int kk = 0; kk < kmax; ++kk) {
-                const int k = j0 + kk, v = k - 1;
-                int pk[2];
-                pk[0] = __shfl_sync(0xffffffffu, pg_l[0], kk);
-                pk[1] = __shfl_sync(0xffffffffu, pg_l[1], kk);
-                if (k < n) {
-                    const int s = k % C::NSK;
-                    if (lane == 0) {
-                        if (k >= C::NSK && !tc::mbar_wait(&kempty[s], ((k / C::NSK) - 1) & 1, abort_flag, kWaitLimit)) {
-                            ok = false;
-                        } else {
-                            pok[k % C::NSC] = (pk[0] >= 0 ? 1 : 0) | (pk[1] >= 0 ? 2 : 0);
-                            tc::mbar_arrive_expect_tx(&kfull[s], ((pk[0] >= 0) + (pk[1] >= 0)) * (C::PAGE + kScalePage * 4));
-                        }
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    if (lane < 4) {
-                        const int p = lane & 1, pg = pk[p];
-                        const int64_t ph = (int64_t)pg * a.H_kv + hk;
-                        if (pg >= 0) {
-                            if (lane < 2)
-                                tc::bulk_g2s(smem + C::SM_K + s * C::TILE + p * C::PAGE, a.k_pages + ph * C::PAGE, C::PAGE,
-                                             &kfull[s]);
-                            else
-                                tc::bulk_g2s(sc_ring + ((k % C::NSC) * 2 + p) * kScalePage, a.kv_scales + ph * kScalePage,
-                                             kScalePage * 4, &kfull[s]);
-                        }
-                    }
-                    k_last = k;
-                }
-                if (v >= 0) {
-                    const int s = v % C::NSV;
-                    if (lane == 0) {
-                        if (v >= C::NSV && !tc::mbar_wait(&vempty[s], ((v / C::NSV) - 1) & 1, abort_flag, kWaitLimit))
-                            ok = false;
-                        else
-                            tc::mbar_arrive_expect_tx(&vfull[s], ((pv[0] >= 0) + (pv[1] >= 0)) * C::PAGE);
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    if (lane < 2 && pv[lane] >= 0)
-                        tc::bulk_g2s(smem + C::SM_V + s * C::TILE + lane * C::PAGE,
-                                     a.v_pages + ((int64_t)pv[lane] * a.H_kv + hk) * C::PAGE, C::PAGE, &vfull[s]);
-                    v_last = v;
-                }
-                pv[0] = pk[0];
-                pv[1] = pk[1];
-            }
-        }
-        if (!ok && lane == 0) *abort_flag = 1;
-        // unwinding: every copy this warp started lands before the CTA can exit
-        if ((!ok || *abort_flag) && lane == 0) {
-            for (int s = 0; s < C::NSK; ++s)
-                if (k_last >= s)
-                    tc::mbar_wait_drain(&kfull[s], ((k_last - (k_last - s) % C::NSK) / C::NSK) & 1, kWaitLimit);
-            for (int s = 0; s < C::NSV; ++s)
-                if (v_last >= s)
-                    tc::mbar_wait_drain(&vfull[s], ((v_last - (v_last - s) % C::NSV) / C::NSV) & 1, kWaitLimit);
-        }
-        __syncwarp();
+        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag);
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             constexpr uint32_t idesc_qk = idesc_f8(Fmt8<FMT>::mma, Fmt8<BDFP8_E4M3>::mma, C::NQ);
             constexpr uint32_t idesc_pv = idesc_f8(Fmt8<FMT>::mma, Fmt8<BDFP8_E5M2>::mma, C::NP);
-            const uint32_t q_addr = tc::smem_u32(q_op);
-            const uint32_t p_addr = tc::smem_u32(p_op);
-            const uint32_t k_addr = tc::smem_u32(smem + C::SM_K);
-            const uint32_t v_addr = tc::smem_u32(smem + C::SM_V);
+            // keys and queries: 8-row groups 8 D bytes apart, 16-element chunks 128 bytes apart; values: 8-channel
+            // groups 512 bytes apart, 16-slot chunks 128; P: 8-row groups 128 bytes apart, chunks P_CHUNK
+            constexpr uint32_t qk_hi = desc_hi(8 * D), v_hi = desc_hi(512), p_hi = desc_hi(128);
+            const uint32_t q_lo = desc_lo(tc::smem_u32(q_op), 128);
+            const uint32_t p_lo = desc_lo(tc::smem_u32(p_op), C::P_CHUNK);
+            const uint32_t k_lo = desc_lo(tc::smem_u32(smem + C::SM_K), 128);
+            const uint32_t v_lo = desc_lo(tc::smem_u32(smem + C::SM_V), 128);
             // the last commit: its phase completes once every tcgen05 operation issued before it has
             uint64_t* last_bar = nullptr;
             uint32_t last_par = 0;
@@ -319,12 +186,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 const int s = j % C::NSK, buf = j & 1;
                 if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, kWaitLimit)) return false;
                 tc::tc_fence_after();
-                const uint32_t kt = k_addr + s * C::TILE;
-                // key rows: 8-row groups 8 D bytes apart (SBO), 16-element chunks 128 bytes apart (LBO)
+                const uint32_t kt = k_lo + s * (C::TILE / 16), d = tbase + C::T_S + buf * C::NQ;
+                mma_f8<false>(d, kt, qk_hi, q_lo, qk_hi, idesc_qk);
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks)
-                    mma_f8(tbase + C::T_S + buf * C::NQ, tc::smem_desc(kt + ks * 256, 128, 8 * D),
-                           tc::smem_desc(q_addr + ks * 256, 128, 8 * D), idesc_qk, ks > 0);
+                for (int ks = 1; ks < C::KS; ++ks) mma_f8<true>(d, kt + ks * 16, qk_hi, q_lo + ks * 16, qk_hi, idesc_qk);
                 tc::mma_commit(&s_full[buf]);
                 tc::mma_commit(&kempty[s]);
                 // passes on this thread's view of the copied scales and the page flags
@@ -342,13 +207,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 if (!(ok = tc::mbar_wait(&p_ready[buf], (j >> 1) & 1, abort_flag, kWaitLimit))) break;
                 if (!(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit))) break;
                 tc::tc_fence_after();
-                const uint32_t vt = v_addr + s * C::TILE;
-                // V^T: 8-channel groups 512 bytes apart, 16-slot chunks 128 apart; P: 8-row groups 128 bytes
-                // apart.  O^T accumulates over the split's tiles (the softmax warps rescale it).
+                const uint32_t vt = v_lo + s * (C::TILE / 16), pt = p_lo + buf * (C::P_BUF / 16), d = tbase + C::T_O;
+                // O^T accumulates over the split's tiles (the softmax warps rescale it)
+                if (j > 0) mma_f8<true>(d, vt, v_hi, pt, p_hi, idesc_pv);
+                else mma_f8<false>(d, vt, v_hi, pt, p_hi, idesc_pv);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_f8(tbase + C::T_O, tc::smem_desc(vt + (ks >> 1) * C::PAGE + (ks & 1) * 256, 128, 512),
-                           tc::smem_desc(p_addr + buf * C::P_BUF + ks * 2 * C::P_CHUNK, C::P_CHUNK, 128), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
+                for (int ks = 1; ks < 4; ++ks)
+                    mma_f8<true>(d, vt + (ks >> 1) * (C::PAGE / 16) + (ks & 1) * 16, v_hi, pt + ks * 2 * (C::P_CHUNK / 16), p_hi,
+                                 idesc_pv);
                 tc::mma_commit(&o_full[buf]);
                 tc::mma_commit(&vempty[s]);
                 last_bar = &vempty[s];
@@ -372,46 +238,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
 
         // query rows as two E4M3 terms: q 2^(7-e) in [128, 256) for the row's largest, the rest times 16
         for (int r = warp; r < ROWS; r += C::NSW) {
-            constexpr int E = D / 32;              // elements per lane
-            float x[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = 0.0f;
-            if (r < nrows) {
-                const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(a.q + row_of(r0 + r) * D) + lane * (E / 2);
-#pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    const float2 f = __bfloat1622float2(src[i]);
-                    x[2 * i] = f.x;
-                    x[2 * i + 1] = f.y;
-                }
-            }
-            // the largest exponent field of the row (255: an infinity or a NaN)
-            uint32_t ex = 0;
-#pragma unroll
-            for (int i = 0; i < E; ++i) ex = max(ex, (__float_as_uint(x[i]) >> 23) & 0xffu);
-            ex = __reduce_max_sync(0xffffffffu, ex);
-            const int e = min(max((int)ex - 127, -119), 127);
-            const float up = pow2i(7 - e);
-            uint32_t c1w = 0, c2w = 0;
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const float y0 = x[i] * up, y1 = x[i + 1] * up;
-                const uint32_t c = f8x2<BDFP8_E4M3>(y0, y1);
-                const float2 v = tc::e4m3x2_value(c);
-                c1w |= c << (8 * i);
-                c2w |= f8x2<BDFP8_E4M3>((y0 - v.x) * 16.0f, (y1 - v.y) * 16.0f) << (8 * i);
-            }
+            uint32_t c1w, c2w;
+            const float f = split_query<D, 4>(r < nrows ? a.q + row_of(r0 + r) * D : nullptr, lane, a.sm_scale, c1w, c2w);
             const int col = 2 * HG * (r / HG) + r % HG;   // a group's q1 columns, then its q2 columns
-            const int e0 = lane * E;
-            auto put = [&](int c, uint32_t w) {
-                uint8_t* dst = q_op + (c >> 3) * (8 * D) + (e0 >> 4) * 128 + (c & 7) * 16 + (e0 & 15);
-                if constexpr (E == 4) *reinterpret_cast<uint32_t*>(dst) = w;
-                else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
-            };
-            put(col, c1w);
-            put(col + HG, c2w);
-            // a row with an infinity or a NaN gives NaN logits
-            if (lane == 0) lsc[r] = ex == 255u ? __uint_as_float(0x7fc00000u) : a.sm_scale * kLog2e * pow2i(e - 7);
+            put_query<D>(q_op, col, lane, c1w);
+            put_query<D>(q_op, col + HG, lane, c2w);
+            if (lane == 0) lsc[r] = f;
         }
         tc::fence_proxy_async_smem();
         tc::named_bar_sync(1 + C::NSG, 32 * C::NSW);
@@ -454,18 +286,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             }
             float x[HG];
             float* const rw = red + (buf * 4 + qd) * C::RED_Q;
+            uint32_t s12[2 * HG];
+            tc::tmem_ld<2 * HG>(tq + C::T_S + buf * C::NQ + 2 * gb, s12);
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int g0 = 0; g0 < HG; g0 += HB) {
-                uint32_t s1[HB], s2[HB];
-                tc::tmem_ld<HB>(tq + C::T_S + buf * C::NQ + 2 * gb + g0, s1);
-                tc::tmem_ld<HB>(tq + C::T_S + buf * C::NQ + 2 * gb + HG + g0, s2);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int g = 0; g < HB; ++g) {
-                    const float s = fmaf(__uint_as_float(s2[g]), 0.0625f, __uint_as_float(s1[g])) * (ka * lr[g0 + g]);
-                    const bool see = valid && (!MT || (g0 + g >= vis0 && g0 + g < vis1));
-                    x[g0 + g] = see ? s : -INFINITY;
-                }
+            for (int g = 0; g < HG; ++g) {
+                const float s = fmaf(__uint_as_float(s12[HG + g]), 0.0625f, __uint_as_float(s12[g])) * (ka * lr[g]);
+                const bool see = valid && (!MT || (g >= vis0 && g < vis1));
+                x[g] = see ? s : -INFINITY;
             }
             float wm_l = -INFINITY;   // lane hl keeps row hl's maximum over the warp's tokens
 #pragma unroll
@@ -510,24 +338,21 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             }
 #pragma unroll
             for (int g = 0; g < HG; g += 2) {
-                constexpr int H1 = HG > 1 ? 1 : 0;
                 const float p0 = tc::ex2_approx(x[g] - __shfl_sync(0xffffffffu, mz, g));
-                const float p1 = tc::ex2_approx(x[g + H1] - __shfl_sync(0xffffffffu, mz, g + H1));
+                const float p1 = tc::ex2_approx(x[g + 1] - __shfl_sync(0xffffffffu, mz, g + 1));
                 l_part[g] += p0;
-                l_part[g + H1] += p1;
-                // three E5M2 terms of p c: each leaves what it cannot hold (exact in fp16) to the next.
-                // An E5M2 code is the upper byte of the fp16 with its value.
-                __half2 y = __floats2half2_rn(p0 * vy, p1 * vy);
+                l_part[g + 1] += p1;
+                float y0 = p0 * vy, y1 = p1 * vy;
+                if constexpr (MT) {   // a token that another row sees, with a scale that is no number
+                    y0 = x[g] == -INFINITY ? 0.0f : y0;
+                    y1 = x[g + 1] == -INFINITY ? 0.0f : y1;
+                }
+                uint32_t c[3];
+                e5m2_terms(__floats2half2_rn(y0, y1), c);
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
-                    uint16_t c;
-                    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<uint32_t*>(&y)));
-                    pb[(k * HG + g) * 16] = (uint8_t)c;
-                    pb[(k * HG + g + H1) * 16] = (uint8_t)(c >> 8);
-                    if (k < 2) {
-                        const uint32_t back = __byte_perm((uint32_t)c, 0u, 0x1404);
-                        y = __hsub2(y, *reinterpret_cast<const __half2*>(&back));
-                    }
+                    pb[(k * HG + g) * 16] = (uint8_t)(c[k] >> 8);
+                    pb[(k * HG + g + 1) * 16] = (uint8_t)(c[k] >> 24);
                 }
             }
             // O^T of the group's rows moves to the new maximum (and scale bound) once the previous
@@ -674,7 +499,7 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_p
 // ------------------------------------------------------------------ host
 inline int rows_for(int G, int64_t T_q) {
     const int64_t rows = G * T_q;
-    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : kWideRows;
 }
 inline int ctas_per_sm(int rows) { return rows <= 8 ? 3 : rows == 16 ? 2 : 1; }
 
@@ -688,18 +513,9 @@ inline int64_t most_tiles(int64_t N, int T_q, int G, int rows, int window, int s
     return std::min(all, win + (sinks + kTileTokens - 1) / kTileTokens);
 }
 
-template <int FMT, int D, int ROWS, bool MT>
-static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
-    using C = Cfg<FMT, D, ROWS, MT>;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
-    if (e != cudaSuccess) {
-        record_cuda_error(e);
-        return BDFP4_ERR_CUDA;
-    }
-    decode_fp8_kernel<FMT, D, ROWS, MT><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
-    const int rc = launch_status();
-    if (rc != BDFP4_OK || a.max_splits <= 1) return rc;
+template <int D>
+static int launch_merge8(const Args& a, int rows_per_cta, cudaStream_t st) {
+    if (a.max_splits <= 1) return BDFP4_OK;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.T_q * a.H_q + 3) / 4));
     cfg.blockDim = dim3(128);
@@ -709,7 +525,7 @@ static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, merge_fp8_kernel<D>, a, ROWS);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, merge_fp8_kernel<D>, a, rows_per_cta);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
@@ -717,22 +533,33 @@ static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
     return launch_status();
 }
 
+template <int FMT, int D, int ROWS, bool MT>
+static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
+    using C = Cfg<FMT, D, ROWS, MT>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return BDFP4_ERR_CUDA;
+    }
+    decode_fp8_kernel<FMT, D, ROWS, MT><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
+    const int rc = launch_status();
+    return rc != BDFP4_OK ? rc : launch_merge8<D>(a, ROWS, st);
+}
+
 template <int FMT, int D>
 static int dispatch(const Args& a, int rows, int64_t ctas, cudaStream_t st) {
-    if (a.T_q > 1) {
-        switch (rows) {
-            case 4: return launch<FMT, D, 4, true>(a, ctas, st);
-            case 8: return launch<FMT, D, 8, true>(a, ctas, st);
-            case 16: return launch<FMT, D, 16, true>(a, ctas, st);
-            default: return launch<FMT, D, 32, true>(a, ctas, st);
-        }
+    if (rows == kWideRows) {
+        const int rc = launch_wide(a, FMT, D, ctas, st);
+        return rc != BDFP4_OK ? rc : launch_merge8<D>(a, kWideRows, st);
     }
-    switch (rows) {
-        case 4: return launch<FMT, D, 4, false>(a, ctas, st);
-        case 8: return launch<FMT, D, 8, false>(a, ctas, st);
-        case 16: return launch<FMT, D, 16, false>(a, ctas, st);
-        default: return launch<FMT, D, 32, false>(a, ctas, st);
-    }
+    if (a.T_q > 1)
+        return rows == 4   ? launch<FMT, D, 4, true>(a, ctas, st)
+               : rows == 8 ? launch<FMT, D, 8, true>(a, ctas, st)
+                           : launch<FMT, D, 16, true>(a, ctas, st);
+    return rows == 4   ? launch<FMT, D, 4, false>(a, ctas, st)
+           : rows == 8 ? launch<FMT, D, 8, false>(a, ctas, st)
+                       : launch<FMT, D, 16, false>(a, ctas, st);
 }
 
 // What every entry point asks of the shape.

@@ -24,8 +24,8 @@
  * A value is its code times its block's scale.  The pages are tcgen05 operands as
  * they stand (K-major, no swizzle: the key tile is the A operand of S^T = K q^T,
  * the value tile that of O^T = V^T P^T), so they go to shared memory with one bulk
- * copy each and are never converted.  Scales have to be finite and below 2^127;
- * bdfp8_append writes powers of two.
+ * copy each and are never converted.  Scales are not negative and below 2^127, or
+ * NaN; bdfp8_append writes powers of two, or NaN with codes of 0.
  *
  * Supported: d in {64, 128}, any H_q that is a multiple of H_kv; other head
  * dims return BDFP4_ERR_UNSUPPORTED.  Cache arrays, kv_scales, the open rows and
@@ -75,7 +75,7 @@ typedef enum { BDFP8_E4M3 = 0, BDFP8_E5M2 = 1 } bdfp8_fmt;
  * smallest power of two, at least 2^-126, with amax <= top s (top = 448 or
  * 57344; s = 1 for a block of zeros), code = x / s to nearest, ties to even.
  * Slots of a written block past the sequence's end become code 0.  A block with
- * an infinity or a NaN gets scale NaN: attention that sees the block is NaN.
+ * an infinity or a NaN gets scale NaN and codes 0: rows that see it are NaN.
  *
  * A block that is not full is quantized again when tokens join it, from the
  * caller-owned open rows, so that a block's bytes do not depend on how its
@@ -126,12 +126,15 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * token of the sequence sees are never read as pages (a streaming cache may have given
  * them back; write -1 or leave them).  Tokens that a row does not see, slots past
  * the end and pages with a bad entry (BDFP4_DEV_BAD_PAGE) have no influence,
- * whatever their bytes and scales.
+ * whatever their bytes and scales; but a value code that is an infinity or a NaN, in a
+ * token that some row of the sequence sees, may reach its other rows too.
  *
  * Arithmetic: a query row is split into two E4M3 terms, exact for a bf16 element
- * down to 2^-13 of the row's largest; logits, softmax and sums are fp32; a
- * probability times its value block's scale goes into the value product as three
- * E5M2 terms (relative error 2^-9, a floor of 2^-32 of the largest).
+ * down to 2^-9 of the row's largest (2^-13 with up to eight rows), to 2^-17 of the
+ * largest below; logits, softmax and sums are fp32; a probability times its value
+ * block's scale goes into the value product as three E5M2 terms (relative error 2^-9,
+ * a floor of 2^-30 of the largest).  G T_q rows of a KV head up to eight take one
+ * kernel, more another that works on 128 rows at a time.
  *
  * An empty sequence and a row that sees no token give zeros; 0 < N_b < T_q also
  * sets BDFP4_DEV_BAD_SEQLEN (rows at negative indexes see nothing), N_b outside

@@ -205,6 +205,19 @@ def test_what_is_not_a_number_reaches_the_rows_that_see_it_only():
         assert not torch.isnan(got).any()
 
 
+@pytest.mark.parametrize("G", [1, 2, 5, 40])
+def test_a_block_that_only_the_newest_query_sees(G):
+    """Its NaN scale, for keys and values, leaves the rows of the earlier query tokens alone."""
+    lens = [193, 65]   # the last token of each begins a block
+    for which in (0, 1):
+        cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 24)
+        for b, n in enumerate(lens):
+            cache.kv_scales[int(bt[b, n // 64]), :, which, 0] = float("nan")
+        q = queries(2, 3, 2 * G, 128, 25)
+        got = decode(q, cache, bt, lens, 1).float().cpu()
+        assert torch.isnan(got[:, 2]).all() and not torch.isnan(got[:, :2]).any()
+
+
 def test_tiny_zero_and_negative():
     """Rows of zeros, of subnormal size, a negative and a zero logit factor."""
     lens = [150, 150, 150]
