@@ -8,11 +8,11 @@
 //  - q = (q1 + q2 / 16) / 2^s: two E4M3 terms.  A bf16 element has 8 significant
 //    bits, an E4M3 term 4, and the rest after rounding to 4 bits fits 4 bits: exact
 //    for elements down to 2^-13 of the row's largest.
-//  - p c = (P1 + P2 + P3) 2^(e-15): three E5M2 terms of what the earlier ones leave.
-//    Each keeps 3 bits (relative error 2^-9 after three, bf16's own 2^-9 on average)
-//    and their common floor is 2^-32 of the largest p c, so a sink with a million
-//    faint tokens behind it keeps their mass (E4M3 terms would be finer, 2^-12, but
-//    end at 2^-26).  2^e bounds the value scales seen so far.
+//  - p c = (P1 + P2 + P3) 2^(ev-11): three E5M2 terms, cut from an fp16 one after another
+//    (e5m2_terms: relative error 2^-9, which is bf16's own on average), with a floor at
+//    2^-28 of the largest, so a sink with a hundred thousand faint tokens behind it keeps
+//    their mass.  (E4M3 terms would be finer, 2^-12, but end at 2^-22.)  2^ev bounds the
+//    value scales seen so far.
 // The terms are stacked as columns of one MMA (N = 2 rows of q, 3 rows of P), S^T =
 // K q^T with M = 128 tokens and O^T = V^T P^T with M = 128 channels.
 //
@@ -33,6 +33,26 @@
 
 namespace bdfp4 {
 namespace fp8 {
+
+// Each row's maximum over the warp, x[g] of the lanes for row g: lane l gets row l % HG's.  Four rows: lanes
+// trade rows in the first two steps, so six shuffles do (a redux.sync for each row took 340 cycles a tile).
+template <int HG>
+__device__ __forceinline__ float rows_max(const float (&x)[HG], int lane) {
+    constexpr uint32_t all = 0xffffffffu;
+    if constexpr (HG == 2) {
+        const float a = tc::redux_max_f32(x[0], all), b = tc::redux_max_f32(x[1], all);
+        return lane & 1 ? b : a;
+    } else {
+        static_assert(HG == 4, "rows");
+        const bool o1 = lane & 1, o2 = lane & 2;
+        const float a = fmaxf(o1 ? x[1] : x[0], __shfl_xor_sync(all, o1 ? x[0] : x[1], 1));
+        const float b = fmaxf(o1 ? x[3] : x[2], __shfl_xor_sync(all, o1 ? x[2] : x[3], 1));
+        float r = fmaxf(o2 ? b : a, __shfl_xor_sync(all, o2 ? a : b, 2));
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) r = fmaxf(r, __shfl_xor_sync(all, r, d));
+        return r;
+    }
+}
 
 template <int FMT, int D, int ROWS, bool MT>
 struct Cfg {
@@ -249,15 +269,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         tc::named_bar_sync(1 + C::NSG, 32 * C::NSW);
         if (lane == 0) tc::mbar_arrive(q_ready);
 
-        // The running maximum of row gb + hl lives in lanes hl, hl + HG, ... of the group's warps, which
-        // compute its terms once; the warp takes them by shuffle.  ev: 2^ev bounds the value scales
-        // seen so far (alike in all threads).
+        // The reference of row gb + hl lives in lanes hl, hl + HG, ... of the group's warps; the warp takes a new one
+        // by shuffle.  ev: 2^ev bounds the value scales seen so far (alike in all threads).
         const int hl = lane % HG;
         float m_l = -INFINITY;
         int ev = -110;
-        float l_part[HG];
+        float l_part[HG], mz[HG];   // mz: the references, 0 where there is none yet
 #pragma unroll
-        for (int g = 0; g < HG; ++g) l_part[g] = 0.0f;
+        for (int g = 0; g < HG; ++g) l_part[g] = mz[g] = 0.0f;
         const int pg = qd >> 1;                                // page of this thread's token in the tile
         const int blk = 2 * (qd & 1) + (lane >> 4);            // its scale block in the page
         const int tok = 32 * qd + lane;
@@ -272,6 +291,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             const int buf = j & 1, t0 = tl.tile(tile0 + j) * kTileTokens;
             if (!tc::mbar_wait(&s_full[buf], (j >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
             tc::tc_fence_after();
+            uint32_t s12[2 * HG];
+            tc::tmem_ld<2 * HG>(tq + C::T_S + buf * C::NQ + 2 * gb, s12);
             const float* sc = sc_ring + ((j % C::NSC) * 2 + pg) * kScalePage + blk;
             const float ka = sc[0], va = sc[kBlocksPerPage];
             const int t = t0 + tok;
@@ -284,26 +305,20 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 vis0 = min(max(d, 0), a.T_q) * a.G - r0 - gb;
                 if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - r0 - gb;
             }
-            float x[HG];
-            float* const rw = red + (buf * 4 + qd) * C::RED_Q;
-            uint32_t s12[2 * HG];
-            tc::tmem_ld<2 * HG>(tq + C::T_S + buf * C::NQ + 2 * gb, s12);
+            // the warp's visible tokens, and the larger of its two blocks' value scales that any of them has
+            const uint32_t seen = __ballot_sync(0xffffffffu, valid);
+            float vmx = (seen >> (lane & 16)) & 0xffffu ? fabsf(va) : 0.0f;
+            vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, 16));
             tc::tmem_wait_ld();
+            float x[HG];
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const float s = fmaf(__uint_as_float(s12[HG + g]), 0.0625f, __uint_as_float(s12[g])) * (ka * lr[g]);
                 const bool see = valid && (!MT || (g >= vis0 && g < vis1));
                 x[g] = see ? s : -INFINITY;
             }
-            float wm_l = -INFINITY;   // lane hl keeps row hl's maximum over the warp's tokens
-#pragma unroll
-            for (int g = 0; g < HG; ++g) {
-                const float wm = tc::redux_max_f32(x[g], 0xffffffffu);
-                wm_l = hl == g ? wm : wm_l;
-            }
-            const float vs = valid ? fabsf(va) : 0.0f;
-            const float vmx = tc::redux_max_f32(vs, 0xffffffffu);
-            const uint32_t seen = __ballot_sync(0xffffffffu, valid);
+            const float wm_l = rows_max<HG>(x, lane);   // row hl's maximum over the warp's tokens
+            float* const rw = red + (buf * 4 + qd) * C::RED_Q;
             if (lane < HG) rw[gb + lane] = wm_l;
             if (lane == 0) {
                 rw[ROWS + grp] = vmx;
@@ -320,26 +335,30 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             const float vt = fmaxf(fmaxf(rr[ROWS + grp], rr[C::RED_Q + ROWS + grp]),
                                    fmaxf(rr[2 * C::RED_Q + ROWS + grp], rr[3 * C::RED_Q + ROWS + grp]));
             const uint4 vm = *reinterpret_cast<const uint4*>(vmask + (buf * C::NSG + grp) * 4);
-            const float mn = fmaxf(m_l, mt);
-            const float mz = mn == -INFINITY ? 0.0f : mn;
-            const float corr_l = tc::ex2_approx(m_l - mz);   // 0 before the first visible token
             // the smallest exponent with |scale| <= 2^ev over what has been seen
             const int en = max(ev, min((int)((__float_as_uint(vt) + 0x7fffffu) >> 23) - 127, 127));
-            const float down = pow2i(max(ev - en, -126));
-            const bool rose = __any_sync(0xffffffffu, mn != m_l || en != ev);
-            m_l = mn;
-            ev = en;
-            // value scale in units of 2^(ev - 15); nothing of a token that no row sees goes in
-            const float vy = valid ? va * pow2i(-en) * 32768.0f : 0.0f;
-            uint8_t* const pb = pslot + buf * C::P_BUF;
+            const bool rise = mt > m_l + kRise;
+            const bool rose = __any_sync(0xffffffffu, rise || en != ev);
+            float corr_l = 1.0f, down = 1.0f;
             if (rose) {
+                corr_l = rise ? tc::ex2_approx(m_l - mt) : 1.0f;   // 0 before the first visible token
+                down = pow2i(max(ev - en, -126));
+                m_l = rise ? mt : m_l;
+                ev = en;
 #pragma unroll
-                for (int g = 0; g < HG; ++g) l_part[g] *= __shfl_sync(0xffffffffu, corr_l, g);
+                for (int g = 0; g < HG; ++g) {
+                    l_part[g] *= __shfl_sync(0xffffffffu, corr_l, g);
+                    const float m = __shfl_sync(0xffffffffu, m_l, g);
+                    mz[g] = m == -INFINITY ? 0.0f : m;
+                }
             }
+            // value scale in units of 2^(ev - kTopExp); nothing of a token that no row sees goes in
+            const float vy = valid ? va * pow2i(-ev) * (float)(1 << kTopExp) : 0.0f;
+            uint8_t* const pb = pslot + buf * C::P_BUF;
 #pragma unroll
             for (int g = 0; g < HG; g += 2) {
-                const float p0 = tc::ex2_approx(x[g] - __shfl_sync(0xffffffffu, mz, g));
-                const float p1 = tc::ex2_approx(x[g + 1] - __shfl_sync(0xffffffffu, mz, g + 1));
+                const float p0 = tc::ex2_approx(x[g] - mz[g]);
+                const float p1 = tc::ex2_approx(x[g + 1] - mz[g + 1]);
                 l_part[g] += p0;
                 l_part[g + 1] += p1;
                 float y0 = p0 * vy, y1 = p1 * vy;
@@ -422,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 if (lane == 0) rl[qd * C::RED_Q + gb + g] = v;
             }
             tc::named_bar_sync(bar_id, 128);
-            const float unit = pow2i(max(ev - 15, -126));
+            const float unit = pow2i(max(ev - kTopExp, -126));
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const int r = gb + g;

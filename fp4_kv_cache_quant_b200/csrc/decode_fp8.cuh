@@ -102,6 +102,13 @@ __device__ __forceinline__ void put_query(uint8_t* op, int row, int lane, uint32
     else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)codes;
 }
 
+// A row's reference for its probabilities follows its maximum only when that has risen by more than kRise (log2
+// units): rescaling O waits for the value product before, and exact maxima rise in four of ten tiles of a split of
+// 32 (four rows a thread).  A probability is then at most 2^kRise; its terms, below 2^15, are in units of
+// 2^-kTopExp, which puts their floor at 2^-28 of the reference.
+constexpr float kRise = 4.0f;
+constexpr int kTopExp = 11;
+
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 
 // The producer warp.  Step k issues the keys and scales of tile k and the values of tile k - 1, so keys run a

@@ -19,20 +19,11 @@
 // free 32 columns, their terms take 24) and two O, 512 columns at D = 128.  (With the
 // probabilities in shared memory a stream's next logits need not wait for its value
 // product, but their stores wait behind the operand reads: 1830 ns a tile.)
-//
-// O is rescaled when a row's maximum rises by more than a factor of four (2 in log2
-// units): a probability is then at most 4, and its terms end at 2^13 instead of 2^15,
-// with their floor at 2^-30 of the largest.
 
 #include "decode_fp8.cuh"
 
 namespace bdfp4 {
 namespace fp8 {
-
-// O is rescaled when a row's maximum rises by more than kRise (log2 units) over its reference, so a probability is
-// at most 2^kRise, and its terms (below 2^15) are in units of 2^-kTopExp.
-constexpr float kRise = 4.0f;
-constexpr int kTopExp = 11;
 
 template <int FMT, int D>
 struct WideCfg {

@@ -133,7 +133,7 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * down to 2^-9 of the row's largest (2^-13 with up to eight rows), to 2^-17 of the
  * largest below; logits, softmax and sums are fp32; a probability times its value
  * block's scale goes into the value product as three E5M2 terms (relative error 2^-9,
- * a floor of 2^-30 of the largest).  G T_q rows of a KV head up to eight take one
+ * a floor of 2^-28 of the largest).  G T_q rows of a KV head up to eight take one
  * kernel, more another that works on 128 rows at a time.
  *
  * An empty sequence and a row that sees no token give zeros; 0 < N_b < T_q also

@@ -66,7 +66,7 @@ def attention(q, K, V, block_table, seq_lens, sm_scale, window=0, sinks=0):
       2 (d + 8) 2^-23 D  the logits' fp32 sums (a whole step per addition), in p and in the sum of p
       (n + 64) 2^-23     the fp32 sums over n tokens
       2^-20              the exponential (2 units of 2^-22 twice) and the final product
-    and n 2^-30 max|v|: the terms' floor, 2^-30 of the largest scaled probability, times a code.
+    and n 2^-28 max|v|: the terms' floor, 2^-28 of the largest scaled probability, times a code.
     The query's terms leave 2^-17 of a row's largest element at the most: with that as an error of every
     q_i, 2 * 2^-17 max|q| sm_scale max_t sum_i |k_ti| in p and in the sum of p."""
     B, T, Hq, d = q.shape
@@ -100,7 +100,7 @@ def attention(q, K, V, block_table, seq_lens, sm_scale, window=0, sinks=0):
                 D += 2.0 ** 23 / (d + 8) * 2.0 ** -17 * np.abs(q[b, i, h]).max() * abs(sm_scale) * np.abs(k).sum(1).max()
                 n = see.sum()
                 rel = 2.0 ** -9 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -23 * D + (n + 64) * 2.0 ** -23 + 2.0 ** -20
-                tol[b, i, h] = 2.0 ** -8 * np.abs(out[b, i, h]) + A * rel + n * 2.0 ** -30 * np.abs(v).max()
+                tol[b, i, h] = 2.0 ** -8 * np.abs(out[b, i, h]) + A * rel + n * 2.0 ** -28 * np.abs(v).max()
     return out, tol
 
 
