@@ -34,8 +34,9 @@
 namespace bdfp4 {
 namespace fp8 {
 
-// Each row's maximum over the warp, x[g] of the lanes for row g: lane l gets row l % HG's.  Four rows: lanes
-// trade rows in the first two steps, so six shuffles do (a redux.sync for each row took 340 cycles a tile).
+// Each row's maximum over the warp, x[g] of the lanes for row g: lane l gets row l % HG's.  Lanes trade rows, half
+// of what they hold in each step, until each holds one (four rows: six shuffles; a redux.sync for each row took
+// 340 cycles a tile).
 template <int HG>
 __device__ __forceinline__ float rows_max(const float (&x)[HG], int lane) {
     constexpr uint32_t all = 0xffffffffu;
@@ -43,14 +44,21 @@ __device__ __forceinline__ float rows_max(const float (&x)[HG], int lane) {
         const float a = tc::redux_max_f32(x[0], all), b = tc::redux_max_f32(x[1], all);
         return lane & 1 ? b : a;
     } else {
-        static_assert(HG == 4, "rows");
-        const bool o1 = lane & 1, o2 = lane & 2;
-        const float a = fmaxf(o1 ? x[1] : x[0], __shfl_xor_sync(all, o1 ? x[0] : x[1], 1));
-        const float b = fmaxf(o1 ? x[3] : x[2], __shfl_xor_sync(all, o1 ? x[2] : x[3], 1));
-        float r = fmaxf(o2 ? b : a, __shfl_xor_sync(all, o2 ? a : b, 2));
+        float r[HG];
 #pragma unroll
-        for (int d = 4; d < 32; d *= 2) r = fmaxf(r, __shfl_xor_sync(all, r, d));
-        return r;
+        for (int g = 0; g < HG; ++g) r[g] = x[g];
+#pragma unroll
+        for (int d = 1, n = HG / 2; d < HG; d *= 2, n /= 2) {   // n rows left: those with bit d of the lane
+            const bool odd = lane & d;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = odd ? r[2 * i + 1] : r[2 * i], give = odd ? r[2 * i] : r[2 * i + 1];
+                r[i] = fmaxf(keep, __shfl_xor_sync(all, give, d));
+            }
+        }
+#pragma unroll
+        for (int d = HG; d < 32; d *= 2) r[0] = fmaxf(r[0], __shfl_xor_sync(all, r[0], d));
+        return r[0];
     }
 }
 
@@ -59,7 +67,7 @@ struct Cfg {
     static constexpr int NQ = 2 * ROWS < 16 ? 16 : 2 * ROWS;      // N of QK: q1 and q2 columns
     static constexpr int NP = (3 * ROWS + 15) / 16 * 16;          // N of PV: three probability terms
     static constexpr int KS = D / 32;                             // MMA K steps of QK
-    static constexpr int NSG = ROWS == 16 ? 4 : 2;                // softmax groups of four warps
+    static constexpr int NSG = 2;                                 // softmax groups of four warps
     static constexpr int HG = ROWS / NSG;                         // rows per group
     static constexpr int NSW = 4 * NSG;
     static constexpr int PRODUCER = NSW, MMA_WARP = NSW + 1;
