@@ -112,6 +112,21 @@ struct Cfg {
     static_assert(ROWS == 4 || ROWS == 8 || ROWS == 16, "more rows take the wide kernel");
 };
 
+constexpr int kMaxCluster = 8;   // blocks of a cluster, the portable limit
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The float at this block's shared address `saddr` in block `rank` of the cluster.
+__device__ __forceinline__ float cluster_ld(uint32_t saddr, int rank) {
+    float v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+                 : "=f"(v)
+                 : "r"(saddr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 template <int FMT, int D, int ROWS, bool MT>
 __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, ROWS, MT>::CTAS)
     decode_fp8_kernel(const Args a) {
@@ -450,6 +465,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             }
             tc::named_bar_sync(bar_id, 128);
             const float unit = pow2i(max(ev - kTopExp, -126));
+            float* const part = reinterpret_cast<float*>(smem);
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const int r = gb + g;
@@ -460,6 +476,9 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 const int64_t row = row_of(r0 + r);
                 if (nspl == 1) {
                     a.out[row * D + chan] = __float2bfloat16(l == 0.0f ? 0.0f : o / l);
+                } else if (a.cluster) {   // the key ring is free: every QK has completed
+                    part[r * D + chan] = o;
+                    if (chan == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * r) = make_float2(m_g, l);
                 } else {
                     a.ws_o[(row * a.max_splits + split) * D + chan] = o;
                     if (chan == 0) {
@@ -477,6 +496,36 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     if (warp == C::MMA_WARP) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tbase, C::T_ALLOC);
+    }
+    // Merge within a cluster: each of the sequence's splits takes a share of the outputs and reads the others'
+    // partial sums where they lie (blocks without a tile have left; they do not count at the barriers).
+    if (a.cluster && nspl > 1) {
+        cluster_sync();
+        const uint32_t part = tc::smem_u32(smem);
+        for (int i = split * C::THREADS + tid; i < nrows * D; i += nspl * C::THREADS) {
+            const int r = i / D;
+            float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], M = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) {
+                if (s >= nspl) break;
+                m[s] = cluster_ld(part + (ROWS * D + 2 * r) * 4, s);
+                l[s] = cluster_ld(part + (ROWS * D + 2 * r + 1) * 4, s);
+                o[s] = cluster_ld(part + i * 4, s);
+            }
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) M = s < nspl ? fmaxf(M, m[s]) : M;
+            if (M == -INFINITY) M = 0.0f;
+            float L = 0.0f, acc = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) {
+                if (s >= nspl) break;
+                const float w = exp2f(m[s] - M);
+                L = fmaf(l[s], w, L);
+                acc = fmaf(o[s], w, acc);
+            }
+            a.out[row_of(r0 + r) * D + i % D] = __float2bfloat16(L == 0.0f ? 0.0f : acc * (1.0f / L));
+        }
+        cluster_sync();   // no block leaves while another reads its sums
     }
 }
 
@@ -569,6 +618,25 @@ static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
     }
+    if (a.cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)a.max_splits;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t le = cudaLaunchKernelEx(&cfg, decode_fp8_kernel<FMT, D, ROWS, MT>, a);
+        if (le != cudaSuccess) {
+            record_cuda_error(le);
+            return BDFP4_ERR_CUDA;
+        }
+        return launch_status();
+    }
     decode_fp8_kernel<FMT, D, ROWS, MT><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
     const int rc = launch_status();
     return rc != BDFP4_OK ? rc : launch_merge8<D>(a, ROWS, st);
@@ -613,26 +681,69 @@ static Shape shape_of(int T_q, int H_q, int H_kv, int max_pages, int window, int
     return s;
 }
 
-// Tiles per split: CTAs of c tiles run in ceil(CTAs / slots) waves of c + 4 tile times (set-up, partial
-// write), and more than one split adds the merge's launch.  tiles_of(b): the tiles a row group
-// of sequence b sees at most.
+// Where the splits of a launch merge: in a cluster when they fit one and all blocks run at once (a cluster's blocks
+// hold their SMs until the last is done, which costs nothing only then), else through the workspace.
+static bool merges_in_cluster(int rows, int max_splits, int64_t ctas, int sms) {
+    return rows <= 16 && max_splits > 1 && max_splits <= kMaxCluster && ctas <= (int64_t)ctas_per_sm(rows) * sms;
+}
+
+// Tiles per split.  The model, in ns: the memory gives a tile (256 D bytes at 6.5 TB/s) to one block after another,
+// and a block takes at least `alone`[k] for a tile of its own with k + 1 blocks on its SM (measured on tiles that
+// come from L2; memory and blocks overlap, but not to the last).  A grid runs in waves of ctas_per_sm blocks an SM, each with
+// a start and an end of about 3.5 us; more than one split adds the merge, 1 us in a cluster or 3 us and
+// the partial sums' traffic.  The plan is the split count of least time, fewer splits on a tie.  tiles_of(b): the
+// tiles that a row group of sequence b sees at most.
 template <class TilesOf>
-static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int ctas) {
-    int64_t most = 1;
-    for (int b = 0; b < B; ++b) most = std::max<int64_t>(most, tiles_of(b));
-    const int64_t slots = (int64_t)std::max(1, sms) * ctas;
-    int64_t best_cost = -1;
-    int best = 1;
-    for (int64_t c = 1; c <= std::min<int64_t>(most, 128); ++c) {
-        int64_t n = 0;
+static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows, int d) {
+    static const float alone4[3] = {900, 1040, 1320}, alone8[3] = {940, 1130, 1570}, alone16[2] = {1020, 1390},
+                       alone128[1] = {1320};
+    const float* alone = rows == 4 ? alone4 : rows == 8 ? alone8 : rows == 16 ? alone16 : alone128;
+    const int ctas = ctas_per_sm(rows);
+    sms = std::max(1, sms);
+    int64_t most = 1, all = 0;
+    for (int b = 0; b < B; ++b) {
+        most = std::max<int64_t>(most, tiles_of(b));
+        all += tiles_of(b);
+    }
+    const double slots = (double)sms * ctas, tile = 256.0 * d / 6500.0, work = (double)all * items * tile;
+    // more than a few waves gain nothing
+    const int64_t s_max = std::min<int64_t>(most, 8 + (int64_t)(4 * slots * most / std::max<double>(1.0, (double)all * items)));
+    double best_cost = -1;
+    int64_t best = most, last = 0;
+    for (int64_t s = 1; s <= s_max; ++s) {
+        const int64_t c = (most + s - 1) / s;
+        if (c == last) continue;
+        last = c;
+        int64_t n = 0, top = 1;
         for (int b = 0; b < B; ++b) n += (tiles_of(b) + c - 1) / c;
-        const int64_t cost = (n * items + slots - 1) / slots * (c + 4) + (c < most ? 4 : 0);
-        if (best_cost < 0 || cost <= best_cost) {
+        n = std::max<int64_t>(1, n * items);
+        top = (most + c - 1) / c;
+        const auto wave = [&](double blocks) {   // blocks at once, at most `slots`
+            const int k = std::min(ctas, std::max(1, (int)((blocks + sms - 1) / sms)));
+            const double mem = work * blocks / n, own = c * (double)alone[k - 1];
+            return std::max(mem, own) + 0.15 * std::min(mem, own) + 3500.0;
+        };
+        const int64_t full = n / (int64_t)slots, rest = n % (int64_t)slots;
+        double cost = full * wave(slots) + (rest ? wave((double)rest) : 0.0);
+        if (top > 1)
+            cost += merges_in_cluster(rows, (int)top, (int64_t)B * items * top, sms) ? 1000.0 : 3000.0 + n * rows * d * 8.0 / 6500.0;
+        if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
-            best = (int)c;
+            best = c;
         }
     }
-    return best;
+    return (int)std::min<int64_t>(best, INT_MAX);
+}
+
+static int sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return BDFP4_ERR_CUDA;
+    static std::atomic<int> known[64];   // per device, as the attribute query costs about a microsecond
+    if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return BDFP4_OK;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return BDFP4_ERR_CUDA;
+    if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return BDFP4_OK;
 }
 
 }  // namespace fp8
@@ -650,7 +761,7 @@ extern "C" int bdfp8_decode_plan(const int32_t* host_seq_lens, int B, int T_q, i
     return plan(
         B,
         [&](int b) { return most_tiles(std::max(0, host_seq_lens[b]), T_q, H_q / H_kv, s.rows, window, sinks); },
-        (int64_t)H_kv * s.groups, num_sms, ctas_per_sm(s.rows));
+        (int64_t)H_kv * s.groups, num_sms, s.rows, d);
 }
 
 static size_t partial_bytes(int64_t rows, int max_splits, int d) {
@@ -687,14 +798,12 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
     a.G = H_q / H_kv;
     a.window = std::min(window, max_pages_per_seq * kPageSlots);
     a.sinks = window > 0 ? std::min(sinks, max_pages_per_seq * kPageSlots) : 0;
+    int sms = 0;
     if (chunk_tiles <= 0) {
-        int dev = 0, sms = 148;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return BDFP4_ERR_CUDA;
+        if ((rc = sm_count(&sms)) != BDFP4_OK) return rc;
         const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, a.window, a.sinks, 1);
         const int64_t tiles = s.max_splits;   // at one tile per split
-        chunk_tiles = plan(1, [&](int) { return tiles; }, (int64_t)B * H_kv * s.groups, sms, ctas_per_sm(s.rows));
+        chunk_tiles = plan(1, [&](int) { return tiles; }, (int64_t)B * H_kv * s.groups, sms, s.rows, d);
     }
     const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, a.window, a.sinks, chunk_tiles);
     a.groups = s.groups;
@@ -710,6 +819,8 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
         a.ws_o = (float*)workspace;
         a.ws_ml = (float*)((char*)workspace + o);
     }
+    if (!sms && (rc = sm_count(&sms)) != BDFP4_OK) return rc;
+    a.cluster = merges_in_cluster(s.rows, s.max_splits, ctas, sms);
     a.q = (const __nv_bfloat16*)q;
     a.k_pages = (const uint8_t*)k_pages;
     a.v_pages = (const uint8_t*)v_pages;

@@ -21,6 +21,7 @@ struct Args {
     __nv_bfloat16* out;
     int32_t* dev_status;
     int B, T_q, H_q, H_kv, G, max_pages, window, sinks, chunk_tiles, max_splits, groups;
+    int cluster;   // 1: the splits of a (sequence, KV head) are a thread block cluster and merge in shared memory
     int64_t num_pages;
     float sm_scale;
 };
