@@ -34,32 +34,28 @@
 namespace bdfp4 {
 namespace fp8 {
 
-// Each row's maximum over the warp, x[g] of the lanes for row g: lane l gets row l % HG's.  Lanes trade rows, half
-// of what they hold in each step, until each holds one (four rows: six shuffles; a redux.sync for each row took
-// 340 cycles a tile).
-template <int HG>
-__device__ __forceinline__ float rows_max(const float (&x)[HG], int lane) {
+// Each row's maximum (or sum) over the warp, x[g] of the lanes for row g: lane l gets row l % HG's.  Lanes trade
+// rows, half of what they hold in each step, until each holds one (four rows: six shuffles; a redux.sync for each
+// row took 340 cycles a tile).
+template <int HG, bool SUM>
+__device__ __forceinline__ float rows_reduce(const float (&x)[HG], int lane) {
     constexpr uint32_t all = 0xffffffffu;
-    if constexpr (HG == 2) {
-        const float a = tc::redux_max_f32(x[0], all), b = tc::redux_max_f32(x[1], all);
-        return lane & 1 ? b : a;
-    } else {
-        float r[HG];
+    auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+    float r[HG];
 #pragma unroll
-        for (int g = 0; g < HG; ++g) r[g] = x[g];
+    for (int g = 0; g < HG; ++g) r[g] = x[g];
 #pragma unroll
-        for (int d = 1, n = HG / 2; d < HG; d *= 2, n /= 2) {   // n rows left: those with bit d of the lane
-            const bool odd = lane & d;
+    for (int d = 1, n = HG / 2; d < HG; d *= 2, n /= 2) {   // n rows left: those with bit d of the lane
+        const bool odd = lane & d;
 #pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float keep = odd ? r[2 * i + 1] : r[2 * i], give = odd ? r[2 * i] : r[2 * i + 1];
-                r[i] = fmaxf(keep, __shfl_xor_sync(all, give, d));
-            }
+        for (int i = 0; i < n; ++i) {
+            const float keep = odd ? r[2 * i + 1] : r[2 * i], give = odd ? r[2 * i] : r[2 * i + 1];
+            r[i] = join(keep, __shfl_xor_sync(all, give, d));
         }
-#pragma unroll
-        for (int d = HG; d < 32; d *= 2) r[0] = fmaxf(r[0], __shfl_xor_sync(all, r[0], d));
-        return r[0];
     }
+#pragma unroll
+    for (int d = HG; d < 32; d *= 2) r[0] = join(r[0], __shfl_xor_sync(all, r[0], d));
+    return r[0];
 }
 
 template <int FMT, int D, int ROWS, bool MT>
@@ -95,7 +91,8 @@ struct Cfg {
     static constexpr int SM_RED = SM_SC + NSC * 2 * kScalePage * 4;           // [2][4][RED_Q]
     static constexpr int SM_VM = (SM_RED + 2 * 4 * RED_Q * 4 + 15) / 16 * 16;   // [2][NSG][4] masks of visible tokens
     static constexpr int SM_LSC = SM_VM + 2 * NSG * 16;                       // [ROWS] logit factors
-    static constexpr int SM_POK = SM_LSC + ROWS * 4;                          // [NSC] page flags
+    static constexpr int SM_ROWS = SM_LSC + ROWS * 4;                         // [ROWS] their rows in the output
+    static constexpr int SM_POK = SM_ROWS + ROWS * 4;                         // [NSC] page flags
     static constexpr int SM_BARS = (SM_POK + NSC * 4 + 7) / 8 * 8;
     static constexpr int NBARS = 2 * NSK + 2 * NSV + 7;
     static constexpr int SM_MISC = SM_BARS + NBARS * 8;
@@ -117,15 +114,6 @@ constexpr int kMaxCluster = 8;   // blocks of a cluster, the portable limit
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The float at this block's shared address `saddr` in block `rank` of the cluster.
-__device__ __forceinline__ float cluster_ld(uint32_t saddr, int rank) {
-    float v;
-    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-                 : "=f"(v)
-                 : "r"(saddr), "r"(rank)
-                 : "memory");
-    return v;
-}
 
 template <int FMT, int D, int ROWS, bool MT>
 __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, ROWS, MT>::CTAS)
@@ -141,6 +129,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     float* const red = reinterpret_cast<float*>(smem + C::SM_RED);
     uint32_t* const vmask = reinterpret_cast<uint32_t*>(smem + C::SM_VM);
     float* const lsc = reinterpret_cast<float*>(smem + C::SM_LSC);
+    int* const rows = reinterpret_cast<int*>(smem + C::SM_ROWS);
     int* const pok = reinterpret_cast<int*>(smem + C::SM_POK);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::SM_BARS);
     uint64_t* const kfull = bars;
@@ -155,27 +144,33 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::SM_MISC + 4);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // row groups of one split stand next to each other: they read the same tiles
-    const int64_t cta = blockIdx.x;
-    const int rg = (int)(cta % a.groups);
-    const int64_t c1 = cta / a.groups;
-    const int split = (int)(c1 % a.max_splits);
-    const int64_t c2 = c1 / a.max_splits;
-    const int hk = (int)(c2 % a.H_kv), b = (int)(c2 / a.H_kv);
-    const int r0 = rg * ROWS, nrows = min(ROWS, a.G * a.T_q - r0);
+    const Place at = place_of(a);
+    const int b = at.b, hk = at.hk, split = at.split;   // one row group
+    const int nrows = a.G * a.T_q;
+    // row of the [B][T_q][H_q] arrays of stacked row r
+    auto row_of = [&](int r) -> int {
+        if constexpr (!MT) return b * a.H_q + hk * a.G + r;
+        return (b * a.T_q + r / a.G) * a.H_q + hk * a.G + r % a.G;
+    };
+    // what does not depend on the sequence's length is loaded while that is on its way
+    int early[2] = {-1, -1};
+    float qx[ROWS > C::NSW ? ROWS / C::NSW : 1][D / 32];
+    if (warp == C::PRODUCER) early_pages(a, at, lane, early);
+    else if (warp < C::NSW)
+#pragma unroll
+        for (int i = 0; i * C::NSW < ROWS; ++i) {
+            const int r = warp + i * C::NSW;
+            load_query<D>(r < nrows ? a.q + (int64_t)row_of(r) * D : nullptr, lane, qx[i]);
+        }
 
     const int N = checked_len(a, b);
-    const Tiles tl = tiles_of(N, a.T_q, a.G, r0, r0 + nrows - 1, a.window, a.sinks);
+    const Tiles tl = tiles_of(N, a.T_q, a.G, 0, nrows - 1, a.window, a.sinks);
     const int nspl = splits_of(tl, a.chunk_tiles);
-    if (tid == 0 && split == 0 && rg == 0 && hk == 0 && (N != a.seq_lens[b] || (N > 0 && N < a.T_q)))
+    if (tid == 0 && split == 0 && hk == 0 && (N != a.seq_lens[b] || (N > 0 && N < a.T_q)))
         set_status(a.dev_status, BDFP4_DEV_BAD_SEQLEN);
-    // row of the [B][T_q][H_q] arrays of stacked row r
-    auto row_of = [&](int r) -> int64_t {
-        return ((int64_t)b * a.T_q + r / a.G) * a.H_q + (int64_t)hk * a.G + r % a.G;
-    };
     if (split > 0 && split >= nspl) return;
     if (tl.total == 0) {
-        for (int i = tid; i < nrows * D; i += C::THREADS) a.out[row_of(r0 + i / D) * D + i % D] = __float2bfloat16(0.0f);
+        for (int i = tid; i < nrows * D; i += C::THREADS) a.out[(int64_t)row_of(i / D) * D + i % D] = __float2bfloat16(0.0f);
         return;
     }
     const int tile0 = split * a.chunk_tiles;
@@ -209,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     const uint32_t tbase = *tmem_slot;
 
     if (warp == C::PRODUCER) {
-        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag);
+        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
@@ -280,13 +275,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         bool bad = false, grp_abort = false;
 
         // query rows as two E4M3 terms: q 2^(7-e) in [128, 256) for the row's largest, the rest times 16
-        for (int r = warp; r < ROWS; r += C::NSW) {
+#pragma unroll
+        for (int i = 0; i * C::NSW < ROWS; ++i) {
+            const int r = warp + i * C::NSW;
+            if (r >= ROWS) break;
             uint32_t c1w, c2w;
-            const float f = split_query<D, 4>(r < nrows ? a.q + row_of(r0 + r) * D : nullptr, lane, a.sm_scale, c1w, c2w);
+            const float f = split_query<D, 4>(qx[i], a.sm_scale, c1w, c2w);
             const int col = 2 * HG * (r / HG) + r % HG;   // a group's q1 columns, then its q2 columns
             put_query<D>(q_op, col, lane, c1w);
             put_query<D>(q_op, col + HG, lane, c2w);
-            if (lane == 0) lsc[r] = f;
+            if (lane == 0) {
+                lsc[r] = f;
+                rows[r] = row_of(r);
+            }
         }
         tc::fence_proxy_async_smem();
         tc::named_bar_sync(1 + C::NSG, 32 * C::NSW);
@@ -325,8 +326,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             [[maybe_unused]] int vis0 = 0, vis1 = HG;
             if constexpr (MT) {
                 const int d = t - (N - a.T_q);
-                vis0 = min(max(d, 0), a.T_q) * a.G - r0 - gb;
-                if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - r0 - gb;
+                vis0 = min(max(d, 0), a.T_q) * a.G - gb;
+                if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - gb;
             }
             // the warp's visible tokens, and the larger of its two blocks' value scales that any of them has
             const uint32_t seen = __ballot_sync(0xffffffffu, valid);
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 const bool see = valid && (!MT || (g >= vis0 && g < vis1));
                 x[g] = see ? s : -INFINITY;
             }
-            const float wm_l = rows_max<HG>(x, lane);   // row hl's maximum over the warp's tokens
+            const float wm_l = rows_reduce<HG, false>(x, lane);   // row hl's maximum over the warp's tokens
             float* const rw = red + (buf * 4 + qd) * C::RED_Q;
             if (lane < HG) rw[gb + lane] = wm_l;
             if (lane == 0) {
@@ -456,16 +457,10 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         if (grp_abort) *abort_flag = 1;
         if (!grp_abort) {
             float* const rl = red;   // [4][RED_Q] partial sums (the maxima are no longer read)
-#pragma unroll
-            for (int g = 0; g < HG; ++g) {
-                float v = l_part[g];
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                if (lane == 0) rl[qd * C::RED_Q + gb + g] = v;
-            }
+            const float l_l = rows_reduce<HG, true>(l_part, lane);
+            if (lane < HG) rl[qd * C::RED_Q + gb + lane] = l_l;
             tc::named_bar_sync(bar_id, 128);
             const float unit = pow2i(max(ev - kTopExp, -126));
-            float* const part = reinterpret_cast<float*>(smem);
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const int r = gb + g;
@@ -473,18 +468,12 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 if (r >= nrows || chan >= D) continue;
                 const float l = (rl[r] + rl[C::RED_Q + r]) + (rl[2 * C::RED_Q + r] + rl[3 * C::RED_Q + r]);
                 const float o = ((__uint_as_float(o3[g]) + __uint_as_float(o2[g])) + __uint_as_float(o1[g])) * unit;
-                const int64_t row = row_of(r0 + r);
+                const int64_t row = rows[r];
                 if (nspl == 1) {
                     a.out[row * D + chan] = __float2bfloat16(l == 0.0f ? 0.0f : o / l);
-                } else if (a.cluster) {   // the key ring is free: every QK has completed
-                    part[r * D + chan] = o;
-                    if (chan == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * r) = make_float2(m_g, l);
                 } else {
                     a.ws_o[(row * a.max_splits + split) * D + chan] = o;
-                    if (chan == 0) {
-                        a.ws_ml[(row * a.max_splits + split) * 2] = m_g;
-                        a.ws_ml[(row * a.max_splits + split) * 2 + 1] = l;
-                    }
+                    if (chan == 0) reinterpret_cast<float2*>(a.ws_ml)[row * a.max_splits + split] = make_float2(m_g, l);
                 }
             }
         }
@@ -497,35 +486,36 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         tc::tc_fence_after();
         tc::tmem_dealloc(tbase, C::T_ALLOC);
     }
-    // Merge within a cluster: each of the sequence's splits takes a share of the outputs and reads the others'
-    // partial sums where they lie (blocks without a tile have left; they do not count at the barriers).
+    // Splits that are a cluster merge here: behind its barrier each takes a share of the outputs (blocks without a
+    // tile have left; they do not count at the barrier).  The partial sums pass through the workspace, which asks for
+    // one barrier; through each other's shared memory it would be two (1400 cycles each).
     if (a.cluster && nspl > 1) {
         cluster_sync();
-        const uint32_t part = tc::smem_u32(smem);
         for (int i = split * C::THREADS + tid; i < nrows * D; i += nspl * C::THREADS) {
-            const int r = i / D;
-            float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], M = -INFINITY;
+            const int64_t row = rows[i / D], at0 = row * a.max_splits;
+            float2 ml[kMaxCluster];
+            float o[kMaxCluster], M = -INFINITY;
 #pragma unroll
             for (int s = 0; s < kMaxCluster; ++s) {
-                if (s >= nspl) break;
-                m[s] = cluster_ld(part + (ROWS * D + 2 * r) * 4, s);
-                l[s] = cluster_ld(part + (ROWS * D + 2 * r + 1) * 4, s);
-                o[s] = cluster_ld(part + i * 4, s);
+                ml[s] = make_float2(-INFINITY, 0.0f);
+                o[s] = 0.0f;
+                if (s < nspl) {
+                    ml[s] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + at0 + s);
+                    o[s] = __ldcg(a.ws_o + (at0 + s) * D + i % D);
+                }
             }
 #pragma unroll
-            for (int s = 0; s < kMaxCluster; ++s) M = s < nspl ? fmaxf(M, m[s]) : M;
+            for (int s = 0; s < kMaxCluster; ++s) M = fmaxf(M, ml[s].x);
             if (M == -INFINITY) M = 0.0f;
             float L = 0.0f, acc = 0.0f;
 #pragma unroll
             for (int s = 0; s < kMaxCluster; ++s) {
-                if (s >= nspl) break;
-                const float w = exp2f(m[s] - M);
-                L = fmaf(l[s], w, L);
+                const float w = tc::ex2_approx(ml[s].x - M);
+                L = fmaf(ml[s].y, w, L);
                 acc = fmaf(o[s], w, acc);
             }
-            a.out[row_of(r0 + r) * D + i % D] = __float2bfloat16(L == 0.0f ? 0.0f : acc * (1.0f / L));
+            a.out[row * D + i % D] = __float2bfloat16(L == 0.0f ? 0.0f : acc * (1.0f / L));
         }
-        cluster_sync();   // no block leaves while another reads its sums
     }
 }
 
@@ -537,10 +527,11 @@ template <int D>
 __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_per_cta) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.T_q * a.H_q) return;
-    const int64_t bt = row / a.H_q;
-    const int h = (int)(row % a.H_q), b = (int)(bt / a.T_q), i = (int)(bt % a.T_q);
+    const unsigned row32 = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row32 >= (unsigned)(a.B * a.T_q * a.H_q)) return;
+    const int64_t row = row32;
+    const unsigned bt = row32 / (unsigned)a.H_q;
+    const int h = row32 % (unsigned)a.H_q, b = bt / (unsigned)a.T_q, i = bt % (unsigned)a.T_q;
     const int r = i * a.G + h % a.G, r0 = r / rows_per_cta * rows_per_cta;
     const Tiles tl = tiles_of(checked_len(a, b), a.T_q, a.G, r0, min(r0 + rows_per_cta, a.G * a.T_q) - 1, a.window, a.sinks);
     const int ns = splits_of(tl, a.chunk_tiles);

@@ -56,13 +56,10 @@ __device__ __forceinline__ int checked_len(const Args& a, int b) {
     return N < 0 || N > a.max_pages * kPageSlots ? 0 : N;
 }
 
-// A query row as two E4M3 terms, by a warp: q 2^(7-e) in [128, 256) for the row's largest element, and
-// the rest times 2^SHIFT.  Returns the factor of the logits (log2 units) that the terms' products carry; a row with
-// an infinity or a NaN gets a NaN.  The lane's D / 32 elements are codes in c1 and c2.  row = null: zeros.
-template <int D, int SHIFT>
-__device__ __forceinline__ float split_query(const __nv_bfloat16* row, int lane, float sm_scale, uint32_t& c1, uint32_t& c2) {
+// The lane's D / 32 elements of a query row (zeros for row = null).
+template <int D>
+__device__ __forceinline__ void load_query(const __nv_bfloat16* row, int lane, float (&x)[D / 32]) {
     constexpr int E = D / 32;
-    float x[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = 0.0f;
     if (row) {
@@ -74,6 +71,14 @@ __device__ __forceinline__ float split_query(const __nv_bfloat16* row, int lane,
             x[2 * i + 1] = f.y;
         }
     }
+}
+
+// A query row as two E4M3 terms, by a warp: q 2^(7-e) in [128, 256) for the row's largest element, and
+// the rest times 2^SHIFT.  Returns the factor of the logits (log2 units) that the terms' products carry; a row with
+// an infinity or a NaN gets a NaN.  x: the lane's elements, whose codes are c1 and c2.
+template <int D, int SHIFT>
+__device__ __forceinline__ float split_query(const float (&x)[D / 32], float sm_scale, uint32_t& c1, uint32_t& c2) {
+    constexpr int E = D / 32;
     // the largest exponent field of the row (255: an infinity or a NaN)
     uint32_t ex = 0;
 #pragma unroll
@@ -112,6 +117,32 @@ constexpr int kTopExp = 11;
 
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 
+// The block's place in a grid of B x H_kv x max_splits x groups: row groups of one split stand next to each
+// other (they read the same tiles), then the splits.
+struct Place {
+    int b, hk, split, rg;
+};
+__device__ __forceinline__ Place place_of(const Args& a) {
+    Place p;
+    unsigned x = blockIdx.x;
+    p.rg = x % (unsigned)a.groups;
+    x /= (unsigned)a.groups;
+    p.split = x % (unsigned)a.max_splits;
+    x /= (unsigned)a.max_splits;
+    p.hk = x % (unsigned)a.H_kv;
+    p.b = x / (unsigned)a.H_kv;
+    return p;
+}
+
+// Without a window a split's pages do not depend on the sequence's length: the producer warp loads the entries of
+// its first 32 tiles while the length is on its way (those within the table; produce uses what the length allows).
+__device__ __forceinline__ void early_pages(const Args& a, const Place& p, int lane, int (&early)[2]) {
+    const int64_t pi = ((int64_t)p.split * a.chunk_tiles + lane) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        early[i] = a.window == 0 && pi + i < a.max_pages ? a.block_table[(int64_t)p.b * a.max_pages + pi + i] : -1;
+}
+
 // The producer warp.  Step k issues the keys and scales of tile k and the values of tile k - 1, so keys run a
 // tile ahead.  Lanes read the page ids of 32 tiles at once; one lane per copy issues.
 // Scales go to slot k % NSC with the keys' byte count.  A key stage is refilled once its QK
@@ -121,7 +152,7 @@ constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 template <class C>
 __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile0, int n, int b, int hk, int lane, uint8_t* smem,
                                         float* sc_ring, int* pok, uint64_t* kfull, uint64_t* kempty, uint64_t* vfull,
-                                        uint64_t* vempty, volatile int* abort_flag) {
+                                        uint64_t* vempty, volatile int* abort_flag, const int (&early)[2]) {
     bool ok = true;
     int pv0 = -1, pv1 = -1;
     int k_last = -1, v_last = -1;
@@ -134,7 +165,7 @@ __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile
                 const int pi = tile * 2 + p, t0 = pi * kPageSlots;
                 // pages that no row sees are not looked up
                 if (t0 < tl.end && (t0 + kPageSlots > tl.lo || t0 < a.sinks)) {
-                    const int v = a.block_table[(int64_t)b * a.max_pages + pi];
+                    const int v = a.window == 0 && j0 == 0 ? early[p] : a.block_table[(int64_t)b * a.max_pages + pi];
                     if (v >= 0 && v < a.num_pages) pg_l[p] = v;
                     else set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
                 }

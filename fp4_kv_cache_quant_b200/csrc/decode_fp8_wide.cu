@@ -123,13 +123,10 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::SM_MISC + 4);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // row groups of one split stand next to each other: they read the same tiles
-    const int64_t cta = blockIdx.x;
-    const int rg = (int)(cta % a.groups);
-    const int64_t c1 = cta / a.groups;
-    const int split = (int)(c1 % a.max_splits);
-    const int64_t c2 = c1 / a.max_splits;
-    const int hk = (int)(c2 % a.H_kv), b = (int)(c2 / a.H_kv);
+    const Place at = place_of(a);
+    const int b = at.b, hk = at.hk, split = at.split, rg = at.rg;
+    int early[2] = {-1, -1};
+    if (warp == C::PRODUCER) early_pages(a, at, lane, early);
     const int r0 = rg * C::ROWS, nrows = min(C::ROWS, a.G * a.T_q - r0);
 
     const int N = checked_len(a, b);
@@ -178,7 +175,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
     const uint32_t tbase = *tmem_slot;
 
     if (warp == C::PRODUCER) {
-        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag);
+        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         // (a warp for each stream, issuing side by side, took 1810 ns a tile)
@@ -261,7 +258,9 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
 #pragma unroll 4
         for (int r = warp; r < C::ROWS; r += C::NSW) {
             uint32_t w1, w2;
-            const float f = split_query<D, 0>(r < nrows ? a.q + row_of(r0 + r) * D : nullptr, lane, a.sm_scale, w1, w2);
+            float x[D / 32];
+            load_query<D>(r < nrows ? a.q + row_of(r0 + r) * D : nullptr, lane, x);
+            const float f = split_query<D, 0>(x, a.sm_scale, w1, w2);
             const uint32_t flip = a.sm_scale < 0.0f ? 0x80808080u : 0u;
             put_query<D>(q_op, r, lane, w1 ^ flip);
             put_query<D>(q_op + C::Q_TERM, r, lane, w2 ^ flip);
