@@ -5,7 +5,10 @@
 // the keys (16 elements of a row each), D for the values (two channels of eight
 // rows each), and all of them for the rotation of the group's queries.  The work is moving bytes
 // (2 B in, 1 B out per key and value element, 2 + 2 per query element); a block's
-// scale needs its maximum first, so its elements wait in registers.
+// scale needs its maximum first, so its elements wait in registers.  With eight CTAs' worth of
+// address arithmetic and a table row for every query head the kernel was bound by issue (143 M
+// warp instructions for 32768 tokens at 32 / 8 heads, 184 us); a thread now keeps its token's cosines and
+// sines for its key and half of the group's query heads.
 //
 // Which sequence a CTA serves: sequence b gets the item numbers f(b) .. f(b+1) - 1,
 // f(b) = cu[b] / 16 + 2 b.  n tokens from any offset touch at most n / 16 + 2 blocks
@@ -39,7 +42,7 @@ struct AppendArgs {
     float* kv_scales;
     int32_t* dev_status;
     int64_t num_pages;
-    int B, T, H_q, H_kv, G, rot, max_pos, adjacent, max_pages;
+    int B, T, H_q, H_kv, G, rot, max_pos, max_pages;
 };
 
 // x cos - y sin to the nearest fp32 but for the last step's rounding: both products' and the
@@ -84,40 +87,62 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     v[1] = *reinterpret_cast<const float4*>(x + 4);
 }
 
+// max(|a|, |b|), a NaN if one is.
+__device__ __forceinline__ float absmax(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
 // A row is handled in units of 16 elements, 8 from ea and 8 from eb, that hold both sides of
 // their rotated pairs and share 8 cosines and sines: with halves paired, elements 8 u.. and 8 u + rot / 2..;
 // else, and behind rot, 16 u.. and 16 u + 8...
 struct Unit {
     int u, ea, eb;
-    __device__ __forceinline__ Unit(int u_, int rot, int adjacent) : u(u_) {
+    __device__ __forceinline__ Unit(int u_, int rot, bool adjacent) : u(u_) {
         const bool halves = !adjacent && 16 * u < rot;
         ea = halves ? 8 * u : 16 * u;
         eb = halves ? 8 * u + (rot >> 1) : 16 * u + 8;
     }
 };
 
-// The unit's elements a[8], b[8] rotated by `cs` (rot / 2 cosines, then as many sines; null = not rotated).
-template <bool EXACT>
-__device__ __forceinline__ void rotate(float* a, float* b, const Unit& un, const float* cs, int rot, int adjacent) {
-    if (!cs || 16 * un.u >= rot) return;
-    auto comb = [](float x, float c, float y, float s) { return EXACT ? turn(x, c, y, s) : fmaf(x, c, -(y * s)); };
+// A unit's cosines and sines: of row `cs` of the table (rot / 2 cosines, then as many sines), or 1 and 0 (cs = null).
+struct Turn {
     float c[8], s[8];
-    load8(cs + 8 * un.u, c);
-    load8(cs + (rot >> 1) + 8 * un.u, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (!adjacent) {
-            const float x = a[i], y = b[i];
-            a[i] = comb(x, c[i], y, s[i]);
-            b[i] = comb(y, c[i], x, -s[i]);
+    __device__ __forceinline__ void load(const float* cs, int u, int rot) {
+        if (cs) {
+            load8(cs + 8 * u, c);
+            load8(cs + (rot >> 1) + 8 * u, s);
         } else {
-            float* const p = (i < 4 ? a : b) + 2 * (i & 3);
-            const float x = p[0], y = p[1];
-            p[0] = comb(x, c[i], y, s[i]);
-            p[1] = comb(y, c[i], x, -s[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = 1.0f;
+                s[i] = 0.0f;
+            }
         }
     }
-}
+    // the unit's elements a[8], b[8]
+    template <bool EXACT, bool ADJ>
+    __device__ __forceinline__ void apply(float* a, float* b) const {
+        auto comb = [](float x, float cc, float y, float ss) { return EXACT ? turn(x, cc, y, ss) : fmaf(x, cc, -(y * ss)); };
+        if constexpr (!ADJ) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = a[i], y = b[i];
+                a[i] = comb(x, c[i], y, s[i]);
+                b[i] = comb(y, c[i], x, -s[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float* const p = (i < 4 ? a : b) + 2 * (i & 3);
+                const float x = p[0], y = p[1];
+                p[0] = comb(x, c[i], y, s[i]);
+                p[1] = comb(y, c[i], x, -s[i]);
+            }
+        }
+    }
+};
 
 // The smallest power of two s >= 2^-126 with amax <= top s, as its exponent; top = 1.75 2^L.
 template <int FMT>
@@ -127,8 +152,8 @@ __device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
     return amax_bits == 0 ? 0 : max(e, -126);
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const AppendArgs a) {
+template <int FMT, int D, bool ADJ>
+__global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const AppendArgs a) {
     constexpr int WK = D / 32;             // warps of the keys, and of the values
     constexpr int UNITS = D / 16;          // units of a row
     constexpr int PAGE = kPageSlots * D;
@@ -178,38 +203,37 @@ __global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const Append
         return a.cos_sin + (int64_t)pos * a.rot;
     };
 
-    // Queries of the group: one unit per thread and step.  The first two steps' loads go out before the
-    // keys and values are worked on.
-    const int q0 = max(mine * kBlockTokens, start), per = a.G * UNITS;
-    const int nq = a.q ? (min((mine + 1) * kBlockTokens, end) - q0) * per : 0;
-    auto q_row = [&](int x, int& t, int& h) {
-        const int i = x / per;
-        t = c0 + q0 + i - start;
-        h = hk * a.G + (x - i * per) / UNITS;
+    // A thread's token of a block and its unit: the first D threads take it of the keys, and both halves of the block
+    // of every other query head of the group, so cosines and sines are loaded once per thread.
+    const int tok = tid / UNITS % kBlockTokens, side = tid / D;
+    const Unit un(tid % UNITS, a.rot, ADJ);
+    const bool turns = 16 * un.u < a.rot;
+    const int my = mine * kBlockTokens + tok;                    // its index in the sequence
+    const bool live = my >= start && my < end;
+    Turn tn;
+    if (turns && live) tn.load(angles(c0 + my - start, my), un.u, a.rot);
+
+    // The queries' first loads go out before the keys and values are worked on.
+    const int64_t t64 = c0 + my - start;
+    const __nv_bfloat16* const q_row = a.q + t64 * a.q_stride + hk * a.G * D;
+    __nv_bfloat16* const q_dst = a.q_out + (t64 * a.H_q + hk * a.G) * D;
+    const int heads = a.q && live ? a.G : 0;
+    auto q_load = [&](int h, uint4* w) {
+        w[0] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.ea));
+        w[1] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.eb));
     };
-    const Unit qu(tid % UNITS, a.rot, a.adjacent);   // alike in every step: 2 D is a multiple of UNITS
-    auto q_load = [&](int x, uint4* w) {
-        int t, h;
-        q_row(x, t, h);
-        const __nv_bfloat16* row = a.q + t * a.q_stride + h * D;
-        w[0] = __ldg(reinterpret_cast<const uint4*>(row + qu.ea));
-        w[1] = __ldg(reinterpret_cast<const uint4*>(row + qu.eb));
-    };
-    auto q_store = [&](int x, const uint4* w) {
-        int t, h;
-        q_row(x, t, h);
+    auto q_store = [&](int h, const uint4* w) {
         float f[8], g[8];
         unpack8(w[0], f);
         unpack8(w[1], g);
-        rotate<false>(f, g, qu, angles(t, start + t - c0), a.rot, a.adjacent);
-        __nv_bfloat16* row = a.q_out + ((int64_t)t * a.H_q + h) * D;
-        *reinterpret_cast<uint4*>(row + qu.ea) = pack8(f);
-        *reinterpret_cast<uint4*>(row + qu.eb) = pack8(g);
+        if (turns) tn.apply<false, ADJ>(f, g);
+        *reinterpret_cast<uint4*>(q_dst + h * D + un.ea) = pack8(f);
+        *reinterpret_cast<uint4*>(q_dst + h * D + un.eb) = pack8(g);
     };
     uint4 qw[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (tid + i * 2 * D < nq) q_load(tid + i * 2 * D, qw[i]);
+        if (side + 2 * i < heads) q_load(side + 2 * i, qw[i]);
 
     // Blocks of this CTA: its own; and, where the sequence's first block has open rows and is not its last,
     // the first block's CTA does the last one too, after it has read the open rows that the last one replaces.
@@ -218,92 +242,111 @@ __global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const Append
     for (int blk = mine;;) {
         if (!(chained && mine == last)) {
             const int i0 = blk * kBlockTokens;                 // first token index of the block
+            const bool whole = i0 >= start && i0 + kBlockTokens <= end;   // all its tokens are new
             const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + i0 / kPageSlots);
             const bool page_ok = page >= 0 && page < a.num_pages;
             if (!page_ok && tid == 0) set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
             const int64_t ph = (int64_t)page * a.H_kv + hk;
             const int slot0 = i0 % kPageSlots;
-            const bool is_v = tid >= D;
-            // keys: row tid / UNITS, one unit; values: channels 2 c and 2 c + 1 of eight rows
-            const int kr = tid / UNITS;
-            const Unit ku(tid % UNITS, a.rot, a.adjacent);
+            // values: channels 2 c and 2 c + 1 of eight rows
             const int vc = tid % (D / 2) * 2, vr = (tid - D) / (D / 2) * 8;
             float x[16];
-            if (!is_v) {
-                const int i = i0 + kr;
-                float* const open = a.k_open + (((int64_t)b * kBlockTokens + kr) * a.H_kv + hk) * D;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-                if (i < start) {
-                    load8(open + ku.ea, x);
-                    load8(open + ku.eb, x + 8);
-                } else if (i < end) {
+            if (side == 0) {
+                const int i = i0 + tok;
+                float* const open = a.k_open + (((int64_t)b * kBlockTokens + tok) * a.H_kv + hk) * D;
+                if (i >= start && i < end) {
                     const int t = c0 + i - start;
                     const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
-                    const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + ku.ea));
-                    const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + ku.eb));
+                    const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + un.ea));
+                    const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + un.eb));
                     unpack8(w0, x);
                     unpack8(w1, x + 8);
-                    rotate<true>(x, x + 8, ku, angles(t, i), a.rot, a.adjacent);
-                    if (blk == last) {
-                        store8(open + ku.ea, x);
-                        store8(open + ku.eb, x + 8);
+                    if (turns) {
+                        if (blk == mine) {
+                            tn.apply<true, ADJ>(x, x + 8);
+                        } else {
+                            Turn other;
+                            other.load(angles(t, i), un.u, a.rot);
+                            other.apply<true, ADJ>(x, x + 8);
+                        }
                     }
+                    if (blk == last) {
+                        store8(open + un.ea, x);
+                        store8(open + un.eb, x + 8);
+                    }
+                } else if (i < start) {
+                    load8(open + un.ea, x);
+                    load8(open + un.eb, x + 8);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
                 }
             } else {
                 uint32_t w[8];
+                __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + vr) * a.H_kv + hk) * D + vc;
+                const int64_t open_step = (int64_t)a.H_kv * D;
+                const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i0 + vr - start) * a.v_stride + hk * D + vc;
+                if (whole) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int i = i0 + vr + r;
-                    __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + vr + r) * a.H_kv + hk) * D + vc;
-                    const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i - start) * a.v_stride + hk * D + vc;
-                    w[r] = i < end ? *reinterpret_cast<const uint32_t*>(i < start ? open : row) : 0u;
+                    for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(row + r * a.v_stride));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int i = i0 + vr + r;
+                        w[r] = 0;
+                        if (i < end) w[r] = *reinterpret_cast<const uint32_t*>(i < start ? open + r * open_step : row + r * a.v_stride);
+                    }
+                }
+                if (blk == last) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int i = i0 + vr + r;
+                        if (i >= start && i < end) *reinterpret_cast<uint32_t*>(open + r * open_step) = w[r];
+                    }
                 }
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int i = i0 + vr + r;
-                    if (blk == last && i >= start && i < end)
-                        *reinterpret_cast<uint32_t*>(a.v_open + (((int64_t)b * kBlockTokens + vr + r) * a.H_kv + hk) * D + vc) = w[r];
                     x[r] = __uint_as_float(w[r] << 16);
                     x[8 + r] = __uint_as_float(w[r] & 0xffff0000u);
                 }
             }
             // as bits, a NaN is above an infinity and that above every number
-            uint32_t mx = 0;
+            float am = absmax(x[0], x[1]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
-            mx = __reduce_max_sync(0xffffffffu, mx);
-            if (lane == 0) red[is_v][warp % WK] = mx;
+            for (int e = 2; e < 16; ++e) am = absmax(am, x[e]);
+            uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+            if (lane == 0) red[side][warp % WK] = mx;
             __syncthreads();
-            mx = red[is_v][0];
+            mx = red[side][0];
 #pragma unroll
-            for (int w = 1; w < WK; ++w) mx = max(mx, red[is_v][w]);
+            for (int w = 1; w < WK; ++w) mx = max(mx, red[side][w]);
             // a block with an infinity or a NaN says so by its scale; its codes are 0, which no product spreads to
             // rows that do not see the block
             const bool finite = mx < 0x7f800000u;
             const int e = scale_exp<FMT>(mx);
             const float inv = pow2i(-e);
             uint2 w[2] = {};
+            if (finite) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float* y = x + 8 * i;
-                if (!finite) continue;
-                w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
-                w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
+                for (int i = 0; i < 2; ++i) {
+                    const float* y = x + 8 * i;
+                    w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
+                    w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
+                }
             }
             if (page_ok) {
-                if (!is_v) {
-                    const int s = slot0 + kr;
+                if (side == 0) {
+                    const int s = slot0 + tok;
                     uint8_t* const dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (s & 7) * 16;
-                    *reinterpret_cast<uint2*>(dst + (ku.ea >> 4) * 128 + (ku.ea & 15)) = w[0];
-                    *reinterpret_cast<uint2*>(dst + (ku.eb >> 4) * 128 + (ku.eb & 15)) = w[1];
+                    *reinterpret_cast<uint2*>(dst + (un.ea >> 4) * 128 + (un.ea & 15)) = w[0];
+                    *reinterpret_cast<uint2*>(dst + (un.eb >> 4) * 128 + (un.eb & 15)) = w[1];
                 } else {
                     uint8_t* const dst = a.v_pages + ph * PAGE + (vc >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (vc & 7) * 16 + vr;
                     *reinterpret_cast<uint2*>(dst) = w[0];
                     *reinterpret_cast<uint2*>(dst + 16) = w[1];
                 }
                 if (tid == 0 || tid == D)
-                    a.kv_scales[ph * kScalePage + (is_v ? kBlocksPerPage : 0) + slot0 / kBlockTokens] =
+                    a.kv_scales[ph * kScalePage + side * kBlocksPerPage + slot0 / kBlockTokens] =
                         finite ? pow2i(e) : __uint_as_float(0x7fc00000u);
             }
         }
@@ -314,15 +357,21 @@ __global__ void __launch_bounds__(2 * D, 512 / D) append_fp8_kernel(const Append
 
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (tid + i * 2 * D < nq) q_store(tid + i * 2 * D, qw[i]);
-    for (int x = tid + 4 * D; x < nq; x += 4 * D) {
+        if (side + 2 * i < heads) q_store(side + 2 * i, qw[i]);
+    for (int h = side + 4; h < heads; h += 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (x + i * 2 * D < nq) q_load(x + i * 2 * D, qw[i]);
+            if (h + 2 * i < heads) q_load(h + 2 * i, qw[i]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (x + i * 2 * D < nq) q_store(x + i * 2 * D, qw[i]);
+            if (h + 2 * i < heads) q_store(h + 2 * i, qw[i]);
     }
+}
+
+template <int FMT, int D>
+static void launch_append(const AppendArgs& a, bool adjacent, unsigned grid, cudaStream_t st) {
+    if (adjacent) append_fp8_kernel<FMT, D, true><<<grid, 2 * D, 0, st>>>(a);
+    else append_fp8_kernel<FMT, D, false><<<grid, 2 * D, 0, st>>>(a);
 }
 
 }  // namespace fp8
@@ -383,16 +432,15 @@ extern "C" int bdfp8_append(const void* k, int64_t k_stride, const void* v, int6
     a.G = H_q / H_kv;
     a.rot = rot_dim;
     a.max_pos = max_pos;
-    a.adjacent = pairing == BDFP8_ROTATE_ADJACENT;
     a.max_pages = max_pages_per_seq;
     cudaStream_t st = (cudaStream_t)stream;
-    const unsigned grid = (unsigned)ctas;
+    const bool adj = pairing == BDFP8_ROTATE_ADJACENT;
     if (fmt == BDFP8_E4M3) {
-        if (d == 128) append_fp8_kernel<BDFP8_E4M3, 128><<<grid, 256, 0, st>>>(a);
-        else append_fp8_kernel<BDFP8_E4M3, 64><<<grid, 128, 0, st>>>(a);
+        if (d == 128) launch_append<BDFP8_E4M3, 128>(a, adj, (unsigned)ctas, st);
+        else launch_append<BDFP8_E4M3, 64>(a, adj, (unsigned)ctas, st);
     } else {
-        if (d == 128) append_fp8_kernel<BDFP8_E5M2, 128><<<grid, 256, 0, st>>>(a);
-        else append_fp8_kernel<BDFP8_E5M2, 64><<<grid, 128, 0, st>>>(a);
+        if (d == 128) launch_append<BDFP8_E5M2, 128>(a, adj, (unsigned)ctas, st);
+        else launch_append<BDFP8_E5M2, 64>(a, adj, (unsigned)ctas, st);
     }
     return launch_status();
 }
