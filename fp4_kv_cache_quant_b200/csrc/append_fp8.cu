@@ -15,6 +15,7 @@
 // (rounded down), which that leaves room for, so f needs no prefix sum: a warp
 // finds b by a 32-way search of cu_tokens.
 
+#include <algorithm>
 #include <climits>
 
 #include "decode_common.cuh"
@@ -42,7 +43,7 @@ struct AppendArgs {
     float* kv_scales;
     int32_t* dev_status;
     int64_t num_pages;
-    int B, T, H_q, H_kv, G, rot, max_pos, max_pages;
+    int B, T, H_q, H_kv, G, rot, max_pos, max_pages, heads_per_cta;
 };
 
 // x cos - y sin to the nearest fp32 but for the last step's rounding: both products' and the
@@ -157,9 +158,11 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     constexpr int WK = D / 32;             // warps of the keys, and of the values
     constexpr int UNITS = D / 16;          // units of a row
     constexpr int PAGE = kPageSlots * D;
-    __shared__ uint32_t red[2][WK];
+    __shared__ uint32_t red[2][2][WK];     // by turns, so that one barrier a block does
+    int turn_of = 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int item = blockIdx.x / a.H_kv, hk = blockIdx.x % a.H_kv;
+    const unsigned head_ctas = (a.H_kv + a.heads_per_cta - 1) / a.heads_per_cta;
+    const int item = blockIdx.x / head_ctas, hk0 = blockIdx.x % head_ctas * a.heads_per_cta;
 
     if (blockIdx.x == 0)   // the sequences that are left out
         for (int b = tid; b < a.B; b += 2 * D) {
@@ -213,158 +216,161 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     Turn tn;
     if (turns && live) tn.load(angles(c0 + my - start, my), un.u, a.rot);
 
-    // The queries' first loads go out before the keys and values are worked on.
-    const int64_t t64 = c0 + my - start;
-    const __nv_bfloat16* const q_row = a.q + t64 * a.q_stride + hk * a.G * D;
-    __nv_bfloat16* const q_dst = a.q_out + (t64 * a.H_q + hk * a.G) * D;
-    const int heads = a.q && live ? a.G : 0;
-    auto q_load = [&](int h, uint4* w) {
-        w[0] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.ea));
-        w[1] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.eb));
-    };
-    auto q_store = [&](int h, const uint4* w) {
-        float f[8], g[8];
-        unpack8(w[0], f);
-        unpack8(w[1], g);
-        if (turns) tn.apply<false, ADJ>(f, g);
-        *reinterpret_cast<uint4*>(q_dst + h * D + un.ea) = pack8(f);
-        *reinterpret_cast<uint4*>(q_dst + h * D + un.eb) = pack8(g);
-    };
-    uint4 qw[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (side + 2 * i < heads) q_load(side + 2 * i, qw[i]);
-
-    // Blocks of this CTA: its own; and, where the sequence's first block has open rows and is not its last,
-    // the first block's CTA does the last one too, after it has read the open rows that the last one replaces.
     const bool reads_open = start % kBlockTokens != 0;
     const bool chained = reads_open && last != blk0;
-    for (int blk = mine;;) {
-        if (!(chained && mine == last)) {
-            const int i0 = blk * kBlockTokens;                 // first token index of the block
-            const bool whole = i0 >= start && i0 + kBlockTokens <= end;   // all its tokens are new
-            const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + i0 / kPageSlots);
-            const bool page_ok = page >= 0 && page < a.num_pages;
-            if (!page_ok && tid == 0) set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
-            const int64_t ph = (int64_t)page * a.H_kv + hk;
-            const int slot0 = i0 % kPageSlots;
-            // values: channels 2 c and 2 c + 1 of eight rows
-            const int vc = tid % (D / 2) * 2, vr = (tid - D) / (D / 2) * 8;
-            float x[16];
-            if (side == 0) {
-                const int i = i0 + tok;
-                float* const open = a.k_open + (((int64_t)b * kBlockTokens + tok) * a.H_kv + hk) * D;
-                if (i >= start && i < end) {
-                    const int t = c0 + i - start;
-                    const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
-                    const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + un.ea));
-                    const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + un.eb));
-                    unpack8(w0, x);
-                    unpack8(w1, x + 8);
-                    if (turns) {
-                        if (blk == mine) {
-                            tn.apply<true, ADJ>(x, x + 8);
-                        } else {
-                            Turn other;
-                            other.load(angles(t, i), un.u, a.rot);
-                            other.apply<true, ADJ>(x, x + 8);
+    for (int hk = hk0; hk < min(hk0 + a.heads_per_cta, a.H_kv); ++hk) {
+        // The queries' first loads go out before the keys and values are worked on.
+        const int64_t t64 = c0 + my - start;
+        const __nv_bfloat16* const q_row = a.q + t64 * a.q_stride + hk * a.G * D;
+        __nv_bfloat16* const q_dst = a.q_out + (t64 * a.H_q + hk * a.G) * D;
+        const int heads = a.q && live ? a.G : 0;
+        auto q_load = [&](int h, uint4* w) {
+            w[0] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.ea));
+            w[1] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.eb));
+        };
+        auto q_store = [&](int h, const uint4* w) {
+            float f[8], g[8];
+            unpack8(w[0], f);
+            unpack8(w[1], g);
+            if (turns) tn.apply<false, ADJ>(f, g);
+            *reinterpret_cast<uint4*>(q_dst + h * D + un.ea) = pack8(f);
+            *reinterpret_cast<uint4*>(q_dst + h * D + un.eb) = pack8(g);
+        };
+        uint4 qw[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (side + 2 * i < heads) q_load(side + 2 * i, qw[i]);
+
+        // Blocks of this CTA: its own; and, where the sequence's first block has open rows and is not its last,
+        // the first block's CTA does the last one too, after it has read the open rows that the last one replaces.
+        for (int blk = mine;;) {
+            if (!(chained && mine == last)) {
+                const int i0 = blk * kBlockTokens;                 // first token index of the block
+                const bool whole = i0 >= start && i0 + kBlockTokens <= end;   // all its tokens are new
+                const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + i0 / kPageSlots);
+                const bool page_ok = page >= 0 && page < a.num_pages;
+                if (!page_ok && tid == 0) set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
+                const int64_t ph = (int64_t)page * a.H_kv + hk;
+                const int slot0 = i0 % kPageSlots;
+                // values: channels 2 c and 2 c + 1 of eight rows
+                const int vc = tid % (D / 2) * 2, vr = (tid - D) / (D / 2) * 8;
+                float x[16];
+                if (side == 0) {
+                    const int i = i0 + tok;
+                    float* const open = a.k_open + (((int64_t)b * kBlockTokens + tok) * a.H_kv + hk) * D;
+                    if (i >= start && i < end) {
+                        const int t = c0 + i - start;
+                        const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
+                        const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + un.ea));
+                        const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + un.eb));
+                        unpack8(w0, x);
+                        unpack8(w1, x + 8);
+                        if (turns) {
+                            if (blk == mine) {
+                                tn.apply<true, ADJ>(x, x + 8);
+                            } else {
+                                Turn other;
+                                other.load(angles(t, i), un.u, a.rot);
+                                other.apply<true, ADJ>(x, x + 8);
+                            }
+                        }
+                        if (blk == last) {
+                            store8(open + un.ea, x);
+                            store8(open + un.eb, x + 8);
+                        }
+                    } else if (i < start) {
+                        load8(open + un.ea, x);
+                        load8(open + un.eb, x + 8);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+                    }
+                } else {
+                    uint32_t w[8];
+                    __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + vr) * a.H_kv + hk) * D + vc;
+                    const int64_t open_step = (int64_t)a.H_kv * D;
+                    const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i0 + vr - start) * a.v_stride + hk * D + vc;
+                    if (whole) {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(row + r * a.v_stride));
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const int i = i0 + vr + r;
+                            w[r] = 0;
+                            if (i < end) w[r] = *reinterpret_cast<const uint32_t*>(i < start ? open + r * open_step : row + r * a.v_stride);
                         }
                     }
                     if (blk == last) {
-                        store8(open + un.ea, x);
-                        store8(open + un.eb, x + 8);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const int i = i0 + vr + r;
+                            if (i >= start && i < end) *reinterpret_cast<uint32_t*>(open + r * open_step) = w[r];
+                        }
                     }
-                } else if (i < start) {
-                    load8(open + un.ea, x);
-                    load8(open + un.eb, x + 8);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-                }
-            } else {
-                uint32_t w[8];
-                __nv_bfloat16* const open = a.v_open + (((int64_t)b * kBlockTokens + vr) * a.H_kv + hk) * D + vc;
-                const int64_t open_step = (int64_t)a.H_kv * D;
-                const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i0 + vr - start) * a.v_stride + hk * D + vc;
-                if (whole) {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(row + r * a.v_stride));
-                } else {
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const int i = i0 + vr + r;
-                        w[r] = 0;
-                        if (i < end) w[r] = *reinterpret_cast<const uint32_t*>(i < start ? open + r * open_step : row + r * a.v_stride);
+                        x[r] = __uint_as_float(w[r] << 16);
+                        x[8 + r] = __uint_as_float(w[r] & 0xffff0000u);
                     }
                 }
-                if (blk == last) {
+                // as bits, a NaN is above an infinity and that above every number
+                float am = absmax(x[0], x[1]);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int i = i0 + vr + r;
-                        if (i >= start && i < end) *reinterpret_cast<uint32_t*>(open + r * open_step) = w[r];
+                for (int e = 2; e < 16; ++e) am = absmax(am, x[e]);
+                uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+                if (lane == 0) red[turn_of][side][warp % WK] = mx;
+                __syncthreads();
+                mx = red[turn_of][side][0];
+#pragma unroll
+                for (int w = 1; w < WK; ++w) mx = max(mx, red[turn_of][side][w]);
+                turn_of ^= 1;
+                // a block with an infinity or a NaN says so by its scale; its codes are 0, which no product spreads to
+                // rows that do not see the block
+                const bool finite = mx < 0x7f800000u;
+                const int e = scale_exp<FMT>(mx);
+                const float inv = pow2i(-e);
+                uint2 w[2] = {};
+                if (finite) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float* y = x + 8 * i;
+                        w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
+                        w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
                     }
                 }
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    x[r] = __uint_as_float(w[r] << 16);
-                    x[8 + r] = __uint_as_float(w[r] & 0xffff0000u);
+                if (page_ok) {
+                    if (side == 0) {
+                        const int s = slot0 + tok;
+                        uint8_t* const dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (s & 7) * 16;
+                        *reinterpret_cast<uint2*>(dst + (un.ea >> 4) * 128 + (un.ea & 15)) = w[0];
+                        *reinterpret_cast<uint2*>(dst + (un.eb >> 4) * 128 + (un.eb & 15)) = w[1];
+                    } else {
+                        uint8_t* const dst = a.v_pages + ph * PAGE + (vc >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (vc & 7) * 16 + vr;
+                        *reinterpret_cast<uint2*>(dst) = w[0];
+                        *reinterpret_cast<uint2*>(dst + 16) = w[1];
+                    }
+                    if (tid == 0 || tid == D)
+                        a.kv_scales[ph * kScalePage + side * kBlocksPerPage + slot0 / kBlockTokens] =
+                            finite ? pow2i(e) : __uint_as_float(0x7fc00000u);
                 }
             }
-            // as bits, a NaN is above an infinity and that above every number
-            float am = absmax(x[0], x[1]);
-#pragma unroll
-            for (int e = 2; e < 16; ++e) am = absmax(am, x[e]);
-            uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
-            if (lane == 0) red[side][warp % WK] = mx;
-            __syncthreads();
-            mx = red[side][0];
-#pragma unroll
-            for (int w = 1; w < WK; ++w) mx = max(mx, red[side][w]);
-            // a block with an infinity or a NaN says so by its scale; its codes are 0, which no product spreads to
-            // rows that do not see the block
-            const bool finite = mx < 0x7f800000u;
-            const int e = scale_exp<FMT>(mx);
-            const float inv = pow2i(-e);
-            uint2 w[2] = {};
-            if (finite) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float* y = x + 8 * i;
-                    w[i].x = f8x2<FMT>(y[0] * inv, y[1] * inv) | (f8x2<FMT>(y[2] * inv, y[3] * inv) << 16);
-                    w[i].y = f8x2<FMT>(y[4] * inv, y[5] * inv) | (f8x2<FMT>(y[6] * inv, y[7] * inv) << 16);
-                }
-            }
-            if (page_ok) {
-                if (side == 0) {
-                    const int s = slot0 + tok;
-                    uint8_t* const dst = a.k_pages + ph * PAGE + (s >> 3) * (8 * D) + (s & 7) * 16;
-                    *reinterpret_cast<uint2*>(dst + (un.ea >> 4) * 128 + (un.ea & 15)) = w[0];
-                    *reinterpret_cast<uint2*>(dst + (un.eb >> 4) * 128 + (un.eb & 15)) = w[1];
-                } else {
-                    uint8_t* const dst = a.v_pages + ph * PAGE + (vc >> 3) * 512 + (slot0 / kBlockTokens) * 128 + (vc & 7) * 16 + vr;
-                    *reinterpret_cast<uint2*>(dst) = w[0];
-                    *reinterpret_cast<uint2*>(dst + 16) = w[1];
-                }
-                if (tid == 0 || tid == D)
-                    a.kv_scales[ph * kScalePage + side * kBlocksPerPage + slot0 / kBlockTokens] =
-                        finite ? pow2i(e) : __uint_as_float(0x7fc00000u);
-            }
+            if (!(chained && blk == blk0)) break;
+            blk = last;
+            __syncthreads();   // the open rows of the first block are read, its maxima too
         }
-        if (!(chained && blk == blk0)) break;
-        blk = last;
-        __syncthreads();   // the open rows of the first block are read, its maxima too
-    }
 
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (side + 2 * i < heads) q_store(side + 2 * i, qw[i]);
-    for (int h = side + 4; h < heads; h += 4) {
-#pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (h + 2 * i < heads) q_load(h + 2 * i, qw[i]);
+            if (side + 2 * i < heads) q_store(side + 2 * i, qw[i]);
+        for (int h = side + 4; h < heads; h += 4) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (h + 2 * i < heads) q_store(h + 2 * i, qw[i]);
+            for (int i = 0; i < 2; ++i)
+                if (h + 2 * i < heads) q_load(h + 2 * i, qw[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (h + 2 * i < heads) q_store(h + 2 * i, qw[i]);
+        }
     }
 }
 
@@ -434,13 +440,18 @@ extern "C" int bdfp8_append(const void* k, int64_t k_stride, const void* v, int6
     a.max_pos = max_pos;
     a.max_pages = max_pages_per_seq;
     cudaStream_t st = (cudaStream_t)stream;
+    // Many blocks: a CTA takes several KV heads of its tokens, which share the search and the table's rows (the second
+    // and third waves of CTAs pay for neither); few: one, for the shortest call.
+    const int64_t items = ctas / H_kv;
+    a.heads_per_cta = ctas >= 4096 ? std::min(4, H_kv) : 1;
+    const unsigned grid = (unsigned)(items * ((H_kv + a.heads_per_cta - 1) / a.heads_per_cta));
     const bool adj = pairing == BDFP8_ROTATE_ADJACENT;
     if (fmt == BDFP8_E4M3) {
-        if (d == 128) launch_append<BDFP8_E4M3, 128>(a, adj, (unsigned)ctas, st);
-        else launch_append<BDFP8_E4M3, 64>(a, adj, (unsigned)ctas, st);
+        if (d == 128) launch_append<BDFP8_E4M3, 128>(a, adj, grid, st);
+        else launch_append<BDFP8_E4M3, 64>(a, adj, grid, st);
     } else {
-        if (d == 128) launch_append<BDFP8_E5M2, 128>(a, adj, (unsigned)ctas, st);
-        else launch_append<BDFP8_E5M2, 64>(a, adj, (unsigned)ctas, st);
+        if (d == 128) launch_append<BDFP8_E5M2, 128>(a, adj, grid, st);
+        else launch_append<BDFP8_E5M2, 64>(a, adj, grid, st);
     }
     return launch_status();
 }
