@@ -16,7 +16,7 @@
 // The terms are stacked as columns of one MMA (N = 2 rows of q, 3 rows of P), S^T =
 // K q^T with M = 128 tokens and O^T = V^T P^T with M = 128 channels.
 //
-// One CTA per (sequence, KV head, split), for up to eight stacked query rows, the G
+// One CTA per (sequence, KV head, split), for up to 16 stacked query rows, the G
 // T_q (token, head) rows of the KV head (more take decode_fp8_wide.cu): eight softmax
 // warps in two groups that each own half of the rows (thread = token, then thread =
 // channel), a producer warp (bulk copies into a key and a value ring; keys run one
@@ -796,6 +796,7 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
         const int64_t tiles = s.max_splits;   // at one tile per split
         chunk_tiles = plan(1, [&](int) { return tiles; }, (int64_t)B * H_kv * s.groups, sms, s.rows, d);
     }
+    chunk_tiles = std::min(chunk_tiles, 1 << 24);   // more than any sequence's tiles
     const Shape s = shape_of(T_q, H_q, H_kv, max_pages_per_seq, a.window, a.sinks, chunk_tiles);
     a.groups = s.groups;
     a.max_splits = s.max_splits;

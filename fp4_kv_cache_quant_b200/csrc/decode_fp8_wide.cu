@@ -1,13 +1,13 @@
-// decode_fp8_wide.cu -- the decode over the 8-bit cache for more than eight stacked
+// decode_fp8_wide.cu -- the decode over the 8-bit cache for more than 16 stacked
 // query rows per KV head: several query tokens, wide head groups, prompt chunks.
 //
 // The mathematics is decode_fp8.cu's with rows and tokens exchanged: S = q K^T with
 // M = 128 query rows and N = 128 tokens, O = P V with N = D channels, so a TMEM lane
-// and its thread own a whole row: maxima and sums need no exchange between
-// threads, and a row's probabilities go back into TMEM, where the value product
-// reads them as its A operand.  With up to eight rows the transposed form costs
-// less (it pays per row); its work per row is about eight times this one's, which
-// here is spent for the 128 rows of the tile whether they are filled or not.
+// and its threads own a whole row: sums need no exchange between threads, a maximum
+// one between two, and a row's probabilities go back into TMEM, where the value
+// product reads them as its A operand.  Its time for a tile is the same for one row
+// and for 128 (1315 ns); the transposed form pays by the row (441, 520 and 690 ns at
+// 4, 8 and 16 rows, 1380 at 32).
 // Both q terms add into one S (q2 at q1's scale: an absolute error of 2^-17 of the
 // row's largest element at the most), the three E5M2 terms of p c into one O.
 //
@@ -15,10 +15,13 @@
 // the even and the odd tiles of the same rows, each with a maximum, a sum and an O of
 // its own, joined at the end like two splits: while one works on its logits the tensor
 // cores work for the other.  A stream is two warpgroups, one for each half of a
-// tile's tokens, which exchange a row's maximum through shared memory.  TMEM: two S (the probabilities over them: 32 tokens' logits read
-// free 32 columns, their terms take 24) and two O, 512 columns at D = 128.  (With the
-// probabilities in shared memory a stream's next logits need not wait for its value
-// product, but their stores wait behind the operand reads: 1830 ns a tile.)
+// tile's tokens, which exchange a row's maximum through shared memory.  TMEM: two S
+// (the probabilities over them: 32 tokens' logits read free 32 columns, their terms
+// take 24) and two O, 512 columns at D = 128.  (With the probabilities in shared memory
+// a stream's next logits need not wait for its value product, but the stores wait
+// behind the operand reads: 1830 ns a tile.)  What bounds it: the thread that issues
+// the MMAs.  A tile is 20 of them at 67 cycles (two terms of q, three of p c), beside
+// seven waits and commits of 100 to 200 cycles each.
 
 #include "decode_fp8.cuh"
 

@@ -60,8 +60,8 @@ typedef enum { BDFP8_E4M3 = 0, BDFP8_E5M2 = 1 } bdfp8_fmt;
  * cu_tokens[b] (seq_lens counts them).  Rows from cu_tokens[B] on are not
  * touched.  k [T][H_kv][d], v [T][H_kv][d], q [T][H_q][d] with token strides of
  * k_stride, v_stride, q_stride elements (heads contiguous: column ranges of one
- * projection's output); q_out [T][H_q][d] contiguous; q = q_out = NULL rotates no
- * queries.
+ * projection's output); q_out [T][H_q][d] contiguous, apart from q; q = q_out =
+ * NULL rotates no queries.
  *
  * Rotation: row p of cos_sin [max_pos][rot_dim] fp32 holds rot_dim / 2 cosines,
  * then as many sines, of position p: positions[t] where positions [T] is given,
@@ -130,10 +130,10 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * token that some row of the sequence sees, may reach its other rows too.
  *
  * Arithmetic: a query row is split into two E4M3 terms, exact for a bf16 element
- * down to 2^-9 of the row's largest (2^-13 with up to eight rows), to 2^-17 of the
+ * down to 2^-9 of the row's largest (2^-13 with up to 16 rows), to 2^-17 of the
  * largest below; logits, softmax and sums are fp32; a probability times its value
  * block's scale goes into the value product as three E5M2 terms (relative error 2^-9,
- * a floor of 2^-28 of the largest).  G T_q rows of a KV head up to eight take one
+ * a floor of 2^-28 of the largest).  Up to 16 G T_q rows of a KV head take one
  * kernel, more another that works on 128 rows at a time.
  *
  * An empty sequence and a row that sees no token give zeros; 0 < N_b < T_q also

@@ -111,14 +111,6 @@ def test_binding_refuses_what_the_pointers_would_hide(lib):
             app(**bad)
 
 
-def _cost(lens, T, G, H_kv, sms, c):
-    rows = G * T
-    ctas = 3 if rows <= 8 else 2 if rows <= 16 else 1
-    items = H_kv * -(-rows // 32)
-    n = items * sum(-(-(-(-x // 128)) // c) for x in lens)
-    return n, ctas * sms, items
-
-
 def test_plan_and_workspace(lib):
     # never more tiles than a sequence has, one tile at the least
     assert bdfp8.bdfp8_decode_plan([0, 0], 1, 8, 2, 128, 148) == 1

@@ -132,11 +132,12 @@ def test_window_equals_the_whole_context_when_it_covers_it():
     assert torch.equal(a, decode(q, cache, bt, lens, 1, window=0, sinks=9))
 
 
-def test_bad_pages_are_left_out_and_reported():
+@pytest.mark.parametrize("G", [4, 24])
+def test_bad_pages_are_left_out_and_reported(G):
     lens = [385, 64, 200]
     cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 9)
     bt[0, 1], bt[0, 4], bt[1, 0] = -5, cache.num_pages, 2 ** 31 - 1
-    q = queries(3, 1, 8, 128, 10)
+    q = queries(3, 1, 2 * G, 128, 10)
     for chunk in (1, 4):
         st = _status()
         got = check(decode(q, cache, bt, lens, chunk, status=st), q, cache, bt, lens)
@@ -152,22 +153,24 @@ def test_bad_lengths_give_zeros_and_are_reported():
         assert int(st) == bdfp4.DEV_BAD_SEQLEN
 
 
+@pytest.mark.parametrize("G", [4, 8, 16, 24])
 @pytest.mark.parametrize("spread", [3, 14])
-def test_value_scales_far_apart(spread):
+def test_value_scales_far_apart(spread, G):
     lens = [500, 129]
     cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 13, spread=spread)
-    q = queries(2, 1, 8, 128, 14)
+    q = queries(2, 1, 2 * G, 128, 14)
     for chunk in (1, 5):
         check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
 
 
-def test_a_first_token_with_a_faint_crowd_behind_it():
+@pytest.mark.parametrize("G", [4, 24])
+def test_a_first_token_with_a_faint_crowd_behind_it(G):
     """One token with half the weight, 32767 others sharing the rest: their probabilities are
     2^-15 of the largest and must not be lost."""
     n, d = 32768, 128
     P = n // 64
     kv = torch.zeros((2, P, 1, 64, d))
-    q = torch.zeros((1, 1, 4, d), dtype=torch.bfloat16)
+    q = torch.zeros((1, 1, G, d), dtype=torch.bfloat16)
     q[..., 0] = 1.0
     kv[0, 0, 0, 0, 0] = 10.4   # exp(10.4) = 2^15.0
     kv[1] = torch.randn(kv[1].shape, generator=torch.Generator().manual_seed(1)) * 0.1 + 1.0
@@ -183,10 +186,11 @@ def test_a_first_token_with_a_faint_crowd_behind_it():
         check(decode(q, cache, bt, [n], chunk, scale=1.0), q, cache, bt, [n], scale=1.0)
 
 
-def test_what_is_not_a_number_reaches_the_rows_that_see_it_only():
+@pytest.mark.parametrize("G", [4, 24])
+def test_what_is_not_a_number_reaches_the_rows_that_see_it_only(G):
     lens = [200, 200]
     cache, bt = make_cache(lens, 1, 128, bdfp8.E4M3, 15)
-    q = queries(2, 3, 4, 128, 16)
+    q = queries(2, 3, G, 128, 16)
     q[0, 1, 2, 5] = float("nan")
     q[1, 0, 0, 7] = float("inf")
     got = decode(q, cache, bt, lens, 1).float().cpu()
@@ -198,7 +202,7 @@ def test_what_is_not_a_number_reaches_the_rows_that_see_it_only():
     for which in (0, 1):
         c2 = bdfp8.FP8Cache(cache.k_pages, cache.v_pages, cache.kv_scales.clone(), *list(vars(cache).values())[3:])
         c2.kv_scales[int(bt[0, 0]), 0, which, 2] = float("nan")
-        q = queries(2, 1, 4, 128, 17)
+        q = queries(2, 1, G, 128, 17)
         got = decode(q, c2, bt, lens, 2).float().cpu()
         assert torch.isnan(got[0]).all() and not torch.isnan(got[1]).any()
         got = decode(q, c2, bt, lens, 2, window=100).float().cpu()   # behind the window: no influence
@@ -218,17 +222,39 @@ def test_a_block_that_only_the_newest_query_sees(G):
         assert torch.isnan(got[:, 2]).all() and not torch.isnan(got[:, :2]).any()
 
 
-def test_tiny_zero_and_negative():
+@pytest.mark.parametrize("G", [4, 8, 24])
+def test_tiny_zero_and_negative(G):
     """Rows of zeros, of subnormal size, a negative and a zero logit factor."""
     lens = [150, 150, 150]
     cache, bt = make_cache(lens, 1, 128, bdfp8.E4M3, 18)
-    q = queries(3, 1, 4, 128, 19)
+    q = queries(3, 1, G, 128, 19)
     q[0] = 0
     q[1] *= 2.0 ** -125
     for scale in (0.09, -0.09, 0.0, 1e30):
         if scale == 1e30:
             q[2] *= 2.0 ** -100
         check(decode(q, cache, bt, lens, 1, scale=scale), q, cache, bt, lens, scale=scale)
+
+
+@pytest.mark.parametrize("G", [4, 8, 16])
+@pytest.mark.parametrize("n", [64 * 3, 64 * 10, 64 * 13, 64 * 14 + 9])
+def test_splits_that_merge_in_a_cluster(n, G):
+    """Two to eight splits of a few sequences, some of them shorter."""
+    lens = [n, n // 3, 0]
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 26)
+    q = queries(3, 1, 2 * G, 128, 27)
+    for chunk in (1, 2):
+        check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
+
+
+def test_more_splits_than_a_cluster_and_odd_plans():
+    lens = [3000, 1, 640]
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 28)
+    for G, T in ((4, 1), (8, 1), (16, 1), (24, 1), (4, 7)):
+        l2 = [max(n, T) for n in lens]
+        q = queries(3, T, 2 * G, 128, 29)
+        for chunk in (1, 5, 1000, 2 ** 31 - 1):
+            check(decode(q, cache, bt, l2 if T == 1 else lens, chunk), q, cache, bt, l2 if T == 1 else lens)
 
 
 def test_offsets_beyond_32_bits():
@@ -457,6 +483,16 @@ def test_prompt_then_generation(window, sinks):
         q, _ = lp.append([n] * 3, tail=0)
         lp.check()
         _loop_check(lp, q, lp.lens, window, sinks)
+
+
+def test_a_prompt_in_chunks_that_attend_as_they_arrive():
+    """Chunks of 70 tokens appended and attending causally, to everything and through a window."""
+    lp = Loop(2, 2, 8, 128, bdfp8.E4M3, 128, False, seed=14)
+    for step in range(3):
+        q, _ = lp.append([70, 70], tail=0)
+        lp.check()
+        _loop_check(lp, q, lp.lens, 0, 0, 2)
+        _loop_check(lp, q, lp.lens, 33, 3, 1)
 
 
 def test_a_captured_step_replays_and_streams_do_not_meet():
