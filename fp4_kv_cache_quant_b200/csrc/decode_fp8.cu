@@ -311,26 +311,29 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         for (int g = 0; g < HG; ++g) lr[g] = lsc[gb + g];
         const uint32_t t_o = tq + C::T_O + 3 * gb;             // a group's first, second and third terms
 
-        for (int j = 0; j < n; ++j) {
-            const int buf = j & 1, t0 = tl.tile(tile0 + j) * kTileTokens;
-            if (!tc::mbar_wait(&s_full[buf], (j >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
-            tc::tc_fence_after();
+        // tiles all of whose tokens all rows see need no masks
+        const int all_end = N - a.T_q + 1, all_lo = a.window > 0 ? N - a.window : 0;
+
+        // One tile's logits to probabilities; FULL: every row sees every token of it.  False: a warp of the group gave up.
+        auto tile = [&](auto full_c, int j, int t0, int good) -> bool {
+            constexpr bool full = decltype(full_c)::value;
+            const int buf = j & 1;
             uint32_t s12[2 * HG];
             tc::tmem_ld<2 * HG>(tq + C::T_S + buf * C::NQ + 2 * gb, s12);
             const float* sc = sc_ring + ((j % C::NSC) * 2 + pg) * kScalePage + blk;
             const float ka = sc[0], va = sc[kBlocksPerPage];
             const int t = t0 + tok;
-            const bool valid = t < tl.end && (t >= tl.lo || t < a.sinks) && ((pok[j % C::NSC] >> pg) & 1);
+            const bool valid = full || (t < tl.end && (t >= tl.lo || t < a.sinks) && ((good >> pg) & 1));
             // several query tokens: row r sees t iff r / G >= t - (N - T_q) and, in a window, r / G < t + W - (N - T_q)
             // or t < sinks: rows [vis0, vis1) of the group
             [[maybe_unused]] int vis0 = 0, vis1 = HG;
-            if constexpr (MT) {
+            if constexpr (MT && !full) {
                 const int d = t - (N - a.T_q);
                 vis0 = min(max(d, 0), a.T_q) * a.G - gb;
                 if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - gb;
             }
             // the warp's visible tokens, and the larger of its two blocks' value scales that any of them has
-            const uint32_t seen = __ballot_sync(0xffffffffu, valid);
+            const uint32_t seen = full ? 0xffffffffu : __ballot_sync(0xffffffffu, valid);
             float vmx = (seen >> (lane & 16)) & 0xffffu ? fabsf(va) : 0.0f;
             vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, 16));
             tc::tmem_wait_ld();
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const float s = fmaf(__uint_as_float(s12[HG + g]), 0.0625f, __uint_as_float(s12[g])) * (ka * lr[g]);
-                const bool see = valid && (!MT || (g >= vis0 && g < vis1));
+                const bool see = full || (valid && (!MT || (g >= vis0 && g < vis1)));
                 x[g] = see ? s : -INFINITY;
             }
             const float wm_l = rows_reduce<HG, false>(x, lane);   // row hl's maximum over the warp's tokens
@@ -346,19 +349,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             if (lane < HG) rw[gb + lane] = wm_l;
             if (lane == 0) {
                 rw[ROWS + grp] = vmx;
-                vmask[(buf * C::NSG + grp) * 4 + qd] = seen;
+                if constexpr (!full) vmask[(buf * C::NSG + grp) * 4 + qd] = seen;
             }
             // one decision for the group's four warps, taken by the barrier itself
-            if (tc::named_bar_or(bar_id, 128, bad)) {
-                grp_abort = true;
-                break;
-            }
+            if (tc::named_bar_or(bar_id, 128, bad)) return false;
             const float* const rr = red + buf * 4 * C::RED_Q;
             const float mt = fmaxf(fmaxf(rr[gb + hl], rr[C::RED_Q + gb + hl]),
                                    fmaxf(rr[2 * C::RED_Q + gb + hl], rr[3 * C::RED_Q + gb + hl]));
             const float vt = fmaxf(fmaxf(rr[ROWS + grp], rr[C::RED_Q + ROWS + grp]),
                                    fmaxf(rr[2 * C::RED_Q + ROWS + grp], rr[3 * C::RED_Q + ROWS + grp]));
-            const uint4 vm = *reinterpret_cast<const uint4*>(vmask + (buf * C::NSG + grp) * 4);
             // the smallest exponent with |scale| <= 2^ev over what has been seen
             const int en = max(ev, min((int)((__float_as_uint(vt) + 0x7fffffu) >> 23) - 127, 127));
             const bool rise = mt > m_l + kRise;
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 l_part[g] += p0;
                 l_part[g + 1] += p1;
                 float y0 = p0 * vy, y1 = p1 * vy;
-                if constexpr (MT) {   // a token that another row sees, with a scale that is no number
+                if constexpr (MT && !full) {   // a token that another row sees, with a scale that is no number
                     y0 = x[g] == -INFINITY ? 0.0f : y0;
                     y1 = x[g + 1] == -INFINITY ? 0.0f : y1;
                 }
@@ -417,7 +416,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             }
             // Value columns of tokens that no row sees are zeroed: their bytes may be anything (a NaN code
             // among them), and 0 times NaN is NaN.  One channel per thread of group 0.
-            if (grp == 0 && (vm.x & vm.y & vm.z & vm.w) != 0xffffffffu) {
+            if (!full && grp == 0) {
+                const uint4 vm = *reinterpret_cast<const uint4*>(vmask + (buf * C::NSG + grp) * 4);
                 const int s = j % C::NSV;
                 if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit)) bad = true;
                 const uint32_t w[4] = {vm.x, vm.y, vm.z, vm.w};
@@ -442,6 +442,19 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&p_ready[buf]);
+            return true;
+        };
+
+        for (int j = 0; j < n; ++j) {
+            const int t0 = tl.tile(tile0 + j) * kTileTokens;
+            if (!tc::mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+            tc::tc_fence_after();
+            const int good = pok[j % C::NSC];
+            if (good == 3 && t0 + kTileTokens <= all_end && (t0 >= all_lo || t0 + kTileTokens <= a.sinks))
+                grp_abort = !tile(std::true_type{}, j, t0, good);
+            else
+                grp_abort = !tile(std::false_type{}, j, t0, good);
+            if (grp_abort) break;
         }
         // ------------------------------------------------------------ epilogue (thread = channel)
         uint32_t o1[HG], o2[HG], o3[HG];
@@ -679,14 +692,18 @@ static bool merges_in_cluster(int rows, int max_splits, int64_t ctas, int sms) {
 }
 
 // Tiles per split.  The model, in ns: the memory gives a tile (256 D bytes at 6.5 TB/s) to one block after another,
-// and a block takes at least `alone`[k] for a tile of its own with k + 1 blocks on its SM (measured on tiles that
-// come from L2; memory and blocks overlap, but not to the last).  A grid runs in waves of ctas_per_sm blocks an SM, each with
-// a start and an end of about 3.5 us; more than one split adds the merge, 1 us in a cluster or 3 us and
-// the partial sums' traffic.  The plan is the split count of least time, fewer splits on a tie.  tiles_of(b): the
-// tiles that a row group of sequence b sees at most.
+// and a block takes at least alone[k] for a tile of its own with k + 1 blocks on its SM (measured on tiles that
+// come from L2); the two overlap but for a tenth.  A grid runs in waves of ctas_per_sm blocks an SM, each with a start
+// and an end of 2.5 us (4 us where the blocks are bound by their own work); with lengths that differ the last blocks
+// run on alone; more than one split adds the merge, 1 us in a cluster or 3 us and the partial sums' traffic.  The
+// plan is the split count of least time, fewer splits on a tie.  Measured, us, by tiles a split: 16 x 32768 tokens, 8
+// KV heads, 4 rows 128: 158, 86: 165, 64: 203, 16: 170, 8: 182 (the plan: 86); the same with 16 rows 128: 177,
+// 64: 187, 32: 197 (128); 64 ragged contexts of 4 KV heads 200: 638, 100: 580, 48: 571, 16: 636 (46); 4 x
+// 131072 147: 183, 100: 166, 79: 173, 32: 184 (79).  tiles_of(b): the tiles that a row group of sequence b
+// sees at most.
 template <class TilesOf>
 static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows, int d) {
-    static const float alone4[3] = {900, 1040, 1320}, alone8[3] = {940, 1130, 1570}, alone16[2] = {1020, 1390},
+    static const float alone4[3] = {900, 1030, 1280}, alone8[3] = {930, 1090, 1470}, alone16[2] = {1020, 1330},
                        alone128[1] = {1320};
     const float* alone = rows == 4 ? alone4 : rows == 8 ? alone8 : rows == 16 ? alone16 : alone128;
     const int ctas = ctas_per_sm(rows);
@@ -712,10 +729,11 @@ static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows
         const auto wave = [&](double blocks) {   // blocks at once, at most `slots`
             const int k = std::min(ctas, std::max(1, (int)((blocks + sms - 1) / sms)));
             const double mem = work * blocks / n, own = c * (double)alone[k - 1];
-            return std::max(mem, own) + 0.15 * std::min(mem, own) + 3500.0;
+            return std::max(mem, own) + 0.1 * std::min(mem, own) + (rows <= 8 ? 2500.0 : 4000.0);
         };
         const int64_t full = n / (int64_t)slots, rest = n % (int64_t)slots;
         double cost = full * wave(slots) + (rest ? wave((double)rest) : 0.0);
+        if (full) cost += 0.5 * (1.0 - (double)all / ((double)B * most)) * c * alone[0];
         if (top > 1)
             cost += merges_in_cluster(rows, (int)top, (int64_t)B * items * top, sms) ? 1000.0 : 3000.0 + n * rows * d * 8.0 / 6500.0;
         if (best_cost < 0 || cost < best_cost) {
