@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     constexpr int WK = D / 32;             // warps of the keys, and of the values
     constexpr int UNITS = D / 16;          // units of a row
     constexpr int PAGE = kPageSlots * D;
+    follow_grid();
     __shared__ uint32_t red[2][2][WK];     // by turns, so that one barrier a block does
     int turn_of = 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -375,9 +376,14 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
 }
 
 template <int FMT, int D>
-static void launch_append(const AppendArgs& a, bool adjacent, unsigned grid, cudaStream_t st) {
-    if (adjacent) append_fp8_kernel<FMT, D, true><<<grid, 2 * D, 0, st>>>(a);
-    else append_fp8_kernel<FMT, D, false><<<grid, 2 * D, 0, st>>>(a);
+static int launch_append(const AppendArgs& a, bool adjacent, unsigned grid, cudaStream_t st) {
+    const cudaError_t e = launch_following(adjacent ? append_fp8_kernel<FMT, D, true> : append_fp8_kernel<FMT, D, false>, grid,
+                                           2 * D, 0, 1, st, a);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return BDFP4_ERR_CUDA;
+    }
+    return launch_status();
 }
 
 }  // namespace fp8
@@ -447,12 +453,7 @@ extern "C" int bdfp8_append(const void* k, int64_t k_stride, const void* v, int6
     a.heads_per_cta = ctas >= 4096 ? std::min(4, H_kv) : 1;
     const unsigned grid = (unsigned)(items * ((H_kv + a.heads_per_cta - 1) / a.heads_per_cta));
     const bool adj = pairing == BDFP8_ROTATE_ADJACENT;
-    if (fmt == BDFP8_E4M3) {
-        if (d == 128) launch_append<BDFP8_E4M3, 128>(a, adj, grid, st);
-        else launch_append<BDFP8_E4M3, 64>(a, adj, grid, st);
-    } else {
-        if (d == 128) launch_append<BDFP8_E5M2, 128>(a, adj, grid, st);
-        else launch_append<BDFP8_E5M2, 64>(a, adj, grid, st);
-    }
-    return launch_status();
+    if (fmt == BDFP8_E4M3)
+        return d == 128 ? launch_append<BDFP8_E4M3, 128>(a, adj, grid, st) : launch_append<BDFP8_E4M3, 64>(a, adj, grid, st);
+    return d == 128 ? launch_append<BDFP8_E5M2, 128>(a, adj, grid, st) : launch_append<BDFP8_E5M2, 64>(a, adj, grid, st);
 }

@@ -120,8 +120,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     decode_fp8_kernel(const Args a) {
     using C = Cfg<FMT, D, ROWS, MT>;
     constexpr int HG = C::HG;
-    // the split merge (a programmatic dependent) may be scheduled as CTAs of this grid retire
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    follow_grid();
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const p_op = smem + C::SM_P;
     uint8_t* const q_op = smem + C::SM_Q;
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
 // sums reaches the output.
 template <int D>
 __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_per_cta) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    follow_grid();
     const int lane = threadIdx.x & 31;
     const unsigned row32 = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row32 >= (unsigned)(a.B * a.T_q * a.H_q)) return;
@@ -596,16 +595,8 @@ inline int64_t most_tiles(int64_t N, int T_q, int G, int rows, int window, int s
 template <int D>
 static int launch_merge8(const Args& a, int rows_per_cta, cudaStream_t st) {
     if (a.max_splits <= 1) return BDFP4_OK;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.T_q * a.H_q + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, merge_fp8_kernel<D>, a, rows_per_cta);
+    const cudaError_t e = launch_following(merge_fp8_kernel<D>, (unsigned)(((int64_t)a.B * a.T_q * a.H_q + 3) / 4), 128, 0, 1, st, a,
+                                           rows_per_cta);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
@@ -617,32 +608,19 @@ template <int FMT, int D, int ROWS, bool MT>
 static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
     using C = Cfg<FMT, D, ROWS, MT>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
+    cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
     }
-    if (a.cluster) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)ctas);
-        cfg.blockDim = dim3(C::THREADS);
-        cfg.dynamicSmemBytes = C::SMEM;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)a.max_splits;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t le = cudaLaunchKernelEx(&cfg, decode_fp8_kernel<FMT, D, ROWS, MT>, a);
-        if (le != cudaSuccess) {
-            record_cuda_error(le);
-            return BDFP4_ERR_CUDA;
-        }
-        return launch_status();
+    e = launch_following(decode_fp8_kernel<FMT, D, ROWS, MT>, (unsigned)ctas, C::THREADS, C::SMEM,
+                         a.cluster ? (unsigned)a.max_splits : 1u, st, a);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return BDFP4_ERR_CUDA;
     }
-    decode_fp8_kernel<FMT, D, ROWS, MT><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
     const int rc = launch_status();
+    if (a.cluster) return rc;
     return rc != BDFP4_OK ? rc : launch_merge8<D>(a, ROWS, st);
 }
 

@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t seen_bits(int lo, int end, int window, int s
 template <int FMT, int D>
 __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_kernel(const Args a) {
     using C = WideCfg<FMT, D>;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    follow_grid();
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_op = smem + C::SM_Q;
     float* const sc_ring = reinterpret_cast<float*>(smem + C::SM_SC);
@@ -541,12 +541,13 @@ template <int FMT, int D>
 static int launch_w(const Args& a, int64_t ctas, cudaStream_t st) {
     using C = WideCfg<FMT, D>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(decode_fp8_wide_kernel<FMT, D>, C::SMEM, done);
+    cudaError_t e = allow_smem(decode_fp8_wide_kernel<FMT, D>, C::SMEM, done);
+    if (e == cudaSuccess)
+        e = launch_following(decode_fp8_wide_kernel<FMT, D>, (unsigned)ctas, C::THREADS, C::SMEM, 1, st, a);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
     }
-    decode_fp8_wide_kernel<FMT, D><<<(unsigned)ctas, C::THREADS, C::SMEM, st>>>(a);
     return launch_status();
 }
 
