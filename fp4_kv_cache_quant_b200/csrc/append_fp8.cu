@@ -416,7 +416,7 @@ extern "C" int bdfp8_append(const void* k, int64_t k_stride, const void* v, int6
         return BDFP4_ERR_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) ||
         !aligned(k_open, 128) || !aligned(v_open, 128) || !aligned(k_pages, 128) || !aligned(v_pages, 128) ||
-        !aligned(kv_scales, 128) || !aligned(cu_tokens, 4) || !aligned(seq_lens, 4) ||
+        !aligned(kv_scales, 32) || !aligned(cu_tokens, 4) || !aligned(seq_lens, 4) ||
         !aligned(positions, 4) || !aligned(block_table, 4) || k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
         return BDFP4_ERR_ALIGN;
     AppendArgs a{};

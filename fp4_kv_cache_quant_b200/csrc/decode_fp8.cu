@@ -786,7 +786,7 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
     if (B == 0) return BDFP4_OK;
     if (!q || !k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !out) return BDFP4_ERR_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_pages, 128) || !aligned(v_pages, 128) ||
-        !aligned(kv_scales, 128) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+        !aligned(kv_scales, 32) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return BDFP4_ERR_ALIGN;
     Args a{};
     a.G = H_q / H_kv;

@@ -28,9 +28,9 @@
  * NaN; bdfp8_append writes powers of two, or NaN with codes of 0.
  *
  * Supported: d in {64, 128}, any H_q that is a multiple of H_kv; other head
- * dims return BDFP4_ERR_UNSUPPORTED.  Cache arrays, kv_scales, the open rows and
- * the workspace are 128-byte aligned, q / k / v / outputs 16-byte aligned with
- * token strides that are multiples of 8 elements (BDFP4_ERR_ALIGN).
+ * dims return BDFP4_ERR_UNSUPPORTED.  Pages, the open rows and the workspace are
+ * 128-byte aligned, kv_scales 32-byte, q / k / v / outputs and cos_sin 16-byte,
+ * with token strides that are multiples of 8 elements (BDFP4_ERR_ALIGN).
  */
 #ifndef BDFP8_H
 #define BDFP8_H

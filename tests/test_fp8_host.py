@@ -54,7 +54,7 @@ def _decode(lib, **kw):
     (-1, dict(q=None)), (-1, dict(out=None)), (-1, dict(sc=None)), (-1, dict(B=-1)), (-1, dict(T=0)), (-1, dict(mp=0)),
     (-1, dict(fmt=2)), (-1, dict(w=-1)), (-1, dict(s=-1)), (-1, dict(H_kv=0)), (-1, dict(np=-1)),
     (-2, dict(H_q=7)),
-    (-3, dict(q=_p(0x10008))), (-3, dict(kp=_p(0x10040))), (-3, dict(sc=_p(0x10020))), (-3, dict(bt=_p(0x10002))),
+    (-3, dict(q=_p(0x10008))), (-3, dict(kp=_p(0x10040))), (-3, dict(sc=_p(0x10010))), (-3, dict(bt=_p(0x10002))),
     (-4, dict(d=96)), (-4, dict(d=256)), (-4, dict(mp=(1 << 24) + 1)), (-4, dict(T=1 << 23)), (-4, dict(np=1 << 31)),
     (-6, dict(chunk=1)),                                   # two splits want a workspace
     (-6, dict(chunk=1, ws=A, wb=16)),
@@ -76,7 +76,7 @@ def _append(lib, **kw):
     (-1, dict(qo=None)), (-1, dict(T=-1)), (-1, dict(B=-1)), (-1, dict(fmt=3)), (-1, dict(pair=2)), (-1, dict(rot=-16)),
     (-2, dict(H_q=7)), (-2, dict(rot=24)), (-2, dict(rot=144)), (-2, dict(ks=255)), (-2, dict(qs=512)),
     (-3, dict(k=_p(0x10008))), (-3, dict(ks=260)), (-3, dict(qs=1028)), (-3, dict(ko=_p(0x10010))),
-    (-3, dict(vp=_p(0x10010))),
+    (-3, dict(vp=_p(0x10010))), (-3, dict(sc=_p(0x10010))), (-3, dict(cu=_p(0x10002))), (-3, dict(cs=_p(0x10008))),
     (-4, dict(d=96, ks=192, vs=192, rot=32)), (-4, dict(T=1 << 30, B=1 << 27)),
     (0, dict(T=0)), (0, dict(B=0)),
 ])

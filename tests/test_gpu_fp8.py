@@ -257,6 +257,37 @@ def test_more_splits_than_a_cluster_and_odd_plans():
             check(decode(q, cache, bt, l2 if T == 1 else lens, chunk), q, cache, bt, l2 if T == 1 else lens)
 
 
+def test_sequences_that_share_pages():
+    """A common prefix: the same pages in two sequences' tables, and twice in one's."""
+    lens = [300, 300, 200]
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 30)
+    bt[1, :3] = bt[0, :3]
+    bt[2, 1] = bt[2, 0]
+    q = queries(3, 2, 8, 128, 31)
+    for chunk in (1, 2):
+        check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
+
+
+def test_a_given_stream_and_misaligned_views():
+    lens = [300]
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 32)
+    q = queries(1, 1, 8, 128, 33)
+    want = decode(q, cache, bt, lens, 1)
+    st, out = torch.cuda.Stream(), torch.empty_like(want)
+    qd, btd = q.cuda(), torch.from_numpy(bt).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = bdfp8.workspace_for(1, 1, 8, 2, 128, bt.shape[1], 1)
+    torch.cuda.synchronize()
+    bdfp8.bdfp8_decode(qd, cache, btd, sl, 1 / math.sqrt(128), 1, ws, out, stream=st)
+    st.synchronize()
+    assert torch.equal(out, want)
+    odd = torch.empty(8 * 128 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(1, 1, 8, 128)
+    with pytest.raises(bdfp4.BDFP4Error, match="align"):
+        bdfp8.bdfp8_decode(odd, cache, btd, sl, 0.1, 1, ws, out)
+    with pytest.raises(bdfp4.BDFP4Error, match="workspace"):
+        bdfp8.bdfp8_decode(qd, cache, btd, sl, 0.1, 1, None, out)
+
+
 def test_offsets_beyond_32_bits():
     """Pages at the far end of a cache of more than 4 GB per array."""
     H, d, P = 8, 128, 70000
@@ -405,6 +436,21 @@ def test_append_finds_its_sequence_in_any_batch(B):
     lp.append(r.integers(0, 3, B).tolist())
     lp.append([1] * B)
     lp.check()
+
+
+def test_rows_before_and_behind_the_sequences_are_left_alone():
+    """cu_tokens need not begin at 0 nor end at T."""
+    lp = Loop(2, 1, 1, 64, bdfp8.E4M3, 0, False, seed=15)
+    k = torch.randn((50, 1, 64), generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    qo = torch.full((50, 1, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    bdfp8.bdfp8_append(k.cuda(), k.cuda(), torch.tensor([17, 37, 40], dtype=torch.int32, device="cuda"),
+                       torch.tensor([20, 3], dtype=torch.int32, device="cuda"), torch.from_numpy(lp.bt).cuda(), None, lp.cache,
+                       lp.open, q=k.cuda(), q_out=qo)
+    kn = k.double().numpy()
+    lp.ref.append(0, kn[17:37], kn[17:37])
+    lp.ref.append(1, kn[37:40], kn[37:40])
+    lp.check()
+    assert torch.equal(qo[17:40].cpu(), k[17:40]) and bool((qo[:17] == 3).all()) and bool((qo[40:] == 3).all())
 
 
 def test_given_positions_and_bad_ones():
