@@ -538,15 +538,22 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     }
 }
 
-// Log-sum-exp merge of the splits, one warp per output row (64 or 128 channels):
+// Log-sum-exp merge of the splits, WARPS warps per output row (64 or 128 channels):
 //   out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,  M = max_s m_s.
 // A split whose tokens a row does not see has m = -inf, l = 0 and weight 0; a NaN among the
-// sums reaches the output.
-template <int D>
-__global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_per_cta) {
+// sums reaches the output.  The warps of a row take every WARPS-th split and join their sums in shared memory in
+// the order of the warps.  What bounds it is the latency of a warp's chain of splits (0.36 us each with one warp a
+// row), so a row gets a block while all rows' blocks run at once; with more rows the grid has warps enough, and the
+// joining only costs.  Measured, decode and merge, us, a warp against a block per row: 32 rows, 131072 tokens in 32
+// splits 55.3 / 47.9, 8 rows in 64 splits 34.6 / 22.0; 512 rows in 8 splits 24.8 / 24.0; 2048 rows in 2 splits 53.7 /
+// 56.8, 8192 rows in 2 splits 71.4 / 87.3.
+constexpr int kMergeThreads = 256, kMergeBlocks = 2048 / kMergeThreads;   // blocks that an SM holds at once
+
+template <int D, int WARPS>
+__global__ void __launch_bounds__(kMergeThreads) merge_fp8_kernel(const Args a, int rows_per_cta) {
     follow_grid();
-    const int lane = threadIdx.x & 31;
-    const unsigned row32 = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned row32 = WARPS == 1 ? blockIdx.x * (kMergeThreads / 32) + warp : blockIdx.x;
     if (row32 >= (unsigned)(a.B * a.T_q * a.H_q)) return;
     const int64_t row = row32;
     const unsigned bt = row32 / (unsigned)a.H_q;
@@ -565,8 +572,8 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_p
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     const float* o = a.ws_o + row * a.max_splits * D + lane * E;
-#pragma unroll 4
-    for (int s = 0; s < ns; ++s) {
+#pragma unroll 8
+    for (int s = WARPS == 1 ? 0 : warp; s < ns; s += WARPS) {
         const float2 w2 = ml[s];
         const float w = exp2f(w2.x - M);
         L = fmaf(w2.y, w, L);
@@ -575,6 +582,20 @@ __global__ void __launch_bounds__(128) merge_fp8_kernel(const Args a, int rows_p
         else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o + (int64_t)s * D);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+    }
+    if constexpr (WARPS > 1) {
+        __shared__ float part[WARPS][D], part_l[WARPS];
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+        if (lane == 0) part_l[warp] = L;
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+            L += part_l[w];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += part[w][lane * E + e];
+        }
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * E);
@@ -602,8 +623,12 @@ inline int64_t most_tiles(int64_t N, int T_q, int G, int rows, int window, int s
 template <int D>
 static int launch_merge8(const Args& a, int rows_per_cta, cudaStream_t st) {
     if (a.max_splits <= 1) return BDFP4_OK;
-    const cudaError_t e = launch_following(merge_fp8_kernel<D>, (unsigned)(((int64_t)a.B * a.T_q * a.H_q + 3) / 4), 128, 0, 1, st, a,
-                                           rows_per_cta);
+    const int64_t rows = (int64_t)a.B * a.T_q * a.H_q;
+    constexpr int kWarps = kMergeThreads / 32;
+    const cudaError_t e =
+        a.merge_rows ? launch_following(merge_fp8_kernel<D, 1>, (unsigned)((rows + kWarps - 1) / kWarps), kMergeThreads, 0, 1, st,
+                                        a, rows_per_cta)
+                     : launch_following(merge_fp8_kernel<D, kWarps>, (unsigned)rows, kMergeThreads, 0, 1, st, a, rows_per_cta);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
@@ -677,19 +702,21 @@ static bool merges_in_cluster(int rows, int max_splits, int64_t ctas, int sms) {
 }
 
 // Tiles per split.  The model, in ns: the memory gives a tile (256 D bytes at 6.5 TB/s) to one block after another,
-// and a block takes at least alone[k] for a tile of its own with k + 1 blocks on its SM (measured on tiles that
-// come from L2); the two overlap but for a tenth.  A grid runs in waves of ctas_per_sm blocks an SM, each with a start
-// and an end of 2.5 us (4 us where the blocks are bound by their own work); with lengths that differ the last blocks
-// run on alone; more than one split adds the merge, 1 us in a cluster or 3 us and the partial sums' traffic.  The
-// plan is the split count of least time, fewer splits on a tie.  Measured, us, by tiles a split: 16 x 32768 tokens, 8
-// KV heads, 4 rows 128: 158, 86: 165, 64: 203, 16: 170, 8: 182 (the plan: 86); the same with 16 rows 128: 177,
-// 64: 187, 32: 197 (128); 64 ragged contexts of 4 KV heads 200: 638, 100: 580, 48: 571, 16: 636 (46); 4 x
-// 131072 147: 183, 100: 166, 79: 173, 32: 184 (79).  tiles_of(b): the tiles that a row group of sequence b
-// sees at most.
+// and a block takes at least alone[k] for a tile of its own with k + 1 blocks on its SM; the two overlap but for an
+// eighth.  A grid runs in waves of ctas_per_sm blocks an SM, each with a start and an end of 2.65 us and 0.82 us for
+// every further block of an SM (6.2 us where the blocks are bound by their own work); with lengths that differ the
+// last blocks run on alone; more than one split adds the merge: in a cluster 1.35 us and more for each block on
+// an SM and each split, else 2.8 us, 20 ns a split and the partial sums' traffic.  The constants are fitted to 957
+// measured calls (1 to 128 sequences of 512 to 131072 tokens, 1 to 8 KV heads, 4 to 128 rows, windows, differing
+// lengths), up to 21 splits each: the split count of least modelled time, which is the plan, takes 1% more than
+// the fastest split on average and 23% at worst.  Measured, us, by tiles a split: 131072 tokens, 8 KV heads, 4 rows
+// 128: 112, 64: 61, 32: 48, 16: 56; one KV head 128: 115, 64: 61, 32: 34, 16: 22; 4 x 4096 tokens 32: 30, 8: 12, 4:
+// 13, 1: 19; 64 x 1000 ragged tokens 8: 22, 4: 27, 2: 35.  tiles_of(b): the tiles that a row group of sequence
+// b sees at most.
 template <class TilesOf>
 static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows, int d) {
-    static const float alone4[3] = {900, 1030, 1280}, alone8[3] = {930, 1090, 1470}, alone16[2] = {1020, 1330},
-                       alone128[1] = {1320};
+    static const float alone4[3] = {900, 910, 1330}, alone8[3] = {920, 1090, 1600}, alone16[2] = {980, 1060},
+                       alone128[1] = {1280};
     const float* alone = rows == 4 ? alone4 : rows == 8 ? alone8 : rows == 16 ? alone16 : alone128;
     const int ctas = ctas_per_sm(rows);
     sms = std::max(1, sms);
@@ -714,13 +741,15 @@ static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows
         const auto wave = [&](double blocks) {   // blocks at once, at most `slots`
             const int k = std::min(ctas, std::max(1, (int)((blocks + sms - 1) / sms)));
             const double mem = work * blocks / n, own = c * (double)alone[k - 1];
-            return std::max(mem, own) + 0.1 * std::min(mem, own) + (rows <= 8 ? 2500.0 : 4000.0);
+            return std::max(mem, own) + 0.12 * std::min(mem, own) + (rows <= 8 ? 2650.0 : 6200.0) + 820.0 * (k - 1);
         };
         const int64_t full = n / (int64_t)slots, rest = n % (int64_t)slots;
         double cost = full * wave(slots) + (rest ? wave((double)rest) : 0.0);
         if (full) cost += 0.5 * (1.0 - (double)all / ((double)B * most)) * c * alone[0];
         if (top > 1)
-            cost += merges_in_cluster(rows, (int)top, (int64_t)B * items * top, sms) ? 1000.0 : 3000.0 + n * rows * d * 8.0 / 6500.0;
+            cost += merges_in_cluster(rows, (int)top, (int64_t)B * items * top, sms)
+                        ? 1350.0 + 650.0 * std::min<double>(n, slots) / sms + 55.0 * top
+                        : 2800.0 + 20.0 * top + 0.002 * n * rows * d;
         if (best_cost < 0 || cost < best_cost) {
             best_cost = cost;
             best = c;
@@ -816,6 +845,7 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
     }
     if (!sms && (rc = sm_count(&sms)) != BDFP4_OK) return rc;
     a.cluster = merges_in_cluster(s.rows, s.max_splits, ctas, sms);
+    a.merge_rows = (int64_t)B * T_q * H_q > (int64_t)kMergeBlocks * sms;
     a.q = (const __nv_bfloat16*)q;
     a.k_pages = (const uint8_t*)k_pages;
     a.v_pages = (const uint8_t*)v_pages;

@@ -21,7 +21,8 @@ struct Args {
     __nv_bfloat16* out;
     int32_t* dev_status;
     int B, T_q, H_q, H_kv, G, max_pages, window, sinks, chunk_tiles, max_splits, groups;
-    int cluster;   // 1: the splits of a (sequence, KV head) are a thread block cluster and merge in shared memory
+    int cluster;   // 1: the splits of a (sequence, KV head) are a thread block cluster and merge behind its barrier
+    int merge_rows;   // 1: the merge kernel takes a warp per output row, 0: a block
     int64_t num_pages;
     float sm_scale;
 };

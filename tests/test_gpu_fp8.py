@@ -257,6 +257,19 @@ def test_more_splits_than_a_cluster_and_odd_plans():
             check(decode(q, cache, bt, l2 if T == 1 else lens, chunk), q, cache, bt, l2 if T == 1 else lens)
 
 
+@pytest.mark.parametrize("B, G, T, d, n", [(1, 1, 1, 128, 128 * 37), (2, 4, 1, 64, 128 * 17 + 1), (3, 7, 1, 128, 128 * 9), (45, 28, 1, 128, 300), (45, 28, 1, 64, 300), (41, 30, 1, 128, 128 * 9 - 3)])
+def test_merges_by_a_block_and_by_a_warp_per_row(B, G, T, d, n):
+    """More splits than a block has warps, fewer, uneven ones; rows below and above those that run at once."""
+    lens = [n, n // 2, 1, 0, 129] * 9
+    lens = lens[:B]
+    cache, bt = make_cache(lens, 1, d, bdfp8.E4M3, 34)
+    q = queries(B, T, G, d, 35)
+    for chunk in (1, 2):
+        got = decode(q, cache, bt, lens, chunk)
+        check(got, q, cache, bt, lens)
+        assert torch.equal(got, decode(q, cache, bt, lens, chunk))
+
+
 def test_sequences_that_share_pages():
     """A common prefix: the same pages in two sequences' tables, and twice in one's."""
     lens = [300, 300, 200]
