@@ -179,14 +179,14 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     while (hi - lo > 31) {
         const int step = (hi - lo + 31) >> 5;
         const int at = lo + lane * step;
-        const bool le = at < hi && (lane == 0 || (__ldg(a.cu + at) >> 4) + 2 * at <= item);
+        const bool le = at < hi && (lane == 0 || (a.cu[at] >> 4) + 2 * at <= item);
         const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
         lo += k * step;
         hi = min(hi, lo + step);
     }
     const int mine_b = lo + lane;
-    const int cu_l = mine_b <= hi ? __ldg(a.cu + mine_b) : 0;
-    const int len_l = mine_b < hi ? __ldg(a.seq_lens + mine_b) : 0;
+    const int cu_l = mine_b <= hi ? a.cu[mine_b] : 0;
+    const int len_l = mine_b < hi ? a.seq_lens[mine_b] : 0;
     const int at_l = __popc(__ballot_sync(0xffffffffu, mine_b < hi && (lane == 0 || (cu_l >> 4) + 2 * mine_b <= item))) - 1;
     const int b = lo + at_l;
     const int c0 = __shfl_sync(0xffffffffu, cu_l, at_l), n = __shfl_sync(0xffffffffu, cu_l, at_l + 1) - c0;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     // table row of token t's position (null: not rotated)
     auto angles = [&](int t, int index) -> const float* {
         if (a.rot == 0) return nullptr;
-        const int pos = a.positions ? __ldg(a.positions + t) : index;
+        const int pos = a.positions ? a.positions[t] : index;
         if (pos < 0 || pos >= a.max_pos) {
             set_status(a.dev_status, BDFP8_DEV_BAD_POSITION);
             return nullptr;
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
         __nv_bfloat16* const q_dst = a.q_out + (t64 * a.H_q + hk * a.G) * D;
         const int heads = a.q && live ? a.G : 0;
         auto q_load = [&](int h, uint4* w) {
-            w[0] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.ea));
-            w[1] = __ldg(reinterpret_cast<const uint4*>(q_row + h * D + un.eb));
+            w[0] = *reinterpret_cast<const uint4*>(q_row + h * D + un.ea);
+            w[1] = *reinterpret_cast<const uint4*>(q_row + h * D + un.eb);
         };
         auto q_store = [&](int h, const uint4* w) {
             float f[8], g[8];
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
             if (!(chained && mine == last)) {
                 const int i0 = blk * kBlockTokens;                 // first token index of the block
                 const bool whole = i0 >= start && i0 + kBlockTokens <= end;   // all its tokens are new
-                const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + i0 / kPageSlots);
+                const int page = a.block_table[(int64_t)b * a.max_pages + i0 / kPageSlots];
                 const bool page_ok = page >= 0 && page < a.num_pages;
                 if (!page_ok && tid == 0) set_status(a.dev_status, BDFP4_DEV_BAD_PAGE);
                 const int64_t ph = (int64_t)page * a.H_kv + hk;
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
                     if (i >= start && i < end) {
                         const int t = c0 + i - start;
                         const __nv_bfloat16* row = a.k + t * a.k_stride + hk * D;
-                        const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(row + un.ea));
-                        const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(row + un.eb));
+                        const uint4 w0 = *reinterpret_cast<const uint4*>(row + un.ea);
+                        const uint4 w1 = *reinterpret_cast<const uint4*>(row + un.eb);
                         unpack8(w0, x);
                         unpack8(w1, x + 8);
                         if (turns) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
                     const __nv_bfloat16* const row = a.v + (int64_t)(c0 + i0 + vr - start) * a.v_stride + hk * D + vc;
                     if (whole) {
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(row + r * a.v_stride));
+                        for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint32_t*>(row + r * a.v_stride);
                     } else {
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {

@@ -96,7 +96,8 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 // blocks may be scheduled while that runs, let the next kernel's be scheduled in turn, and wait here, before they
 // read, write or allocate anything (tensor memory held while waiting could be what the grid before needs).  Every
 // block waits, also one without work, so that a grid's end implies the end of the grids before it.  Calls that
-// follow one another on a stream cost about 2 us less each.
+// follow one another on a stream cost about 2 us less each.  What earlier grids may have written is then read with plain
+// loads: one through the read-only path (__ldg) need not stay behind the wait.
 __device__ __forceinline__ void follow_grid() {
     asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;" ::: "memory");
 }
