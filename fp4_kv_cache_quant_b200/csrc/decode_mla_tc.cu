@@ -259,6 +259,8 @@ __global__ void __launch_bounds__(MlaCfg<FMT, GH>::THREADS, 1) decode_mla_tc_ker
     if (N == 0) {
         for (int i = tid; i < GH * C::DV; i += blockDim.x)
             a.out[((int64_t)b * a.H_q + h0 + i / C::DV) * C::DV + i % C::DV] = __float2bfloat16(0.0f);
+        // a grid behind this one may start once all of this one's CTAs have left: not while the prologue runs
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     const int tile0 = split * a.chunk_tiles;

@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(TcCfg<FMT, G>::THREADS, TcCfg<FMT, G>::MIN_CTA
     if (split > 0 && split >= nspl) return;
     if (N == 0) {
         for (int i = tid; i < G * C::DV; i += blockDim.x) a.out[row_of(i / C::DV) * C::DV + i % C::DV] = __float2bfloat16(0.0f);
+        // a grid behind this one may start once all of this one's CTAs have left: not while the prologue runs
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     const int tile0 = split * a.chunk_tiles;

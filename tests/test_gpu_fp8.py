@@ -281,6 +281,30 @@ def test_sequences_that_share_pages():
         check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
 
 
+@pytest.mark.parametrize("d_k, d_v, Hq, H", [(128, 128, 8, 2), (576, 512, 16, 1)])
+def test_behind_an_fp4_decode_of_empty_sequences_in_the_same_workspace(d_k, d_v, Hq, H):
+    """The FP4 decode's query images go to the workspace that the next call's partial sums take."""
+    from fp4_kv_cache_quant_b200 import bdfp4
+    lens, B4 = [700, 200], 64
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 36)
+    q = queries(2, 1, 8, 128, 37)
+    want = decode(q, cache, bt, lens, 1)
+    check(want, q, cache, bt, lens)
+    ones = lambda *s: torch.ones(s, dtype=torch.float32, device="cuda")  # noqa: E731
+    c4, kv = bdfp4.FP4Cache.empty(4, H, d_k, d_v, bdfp4.NVFP4), bdfp4.KVParams(ones(H, d_k), ones(H), ones(H))
+    q4 = torch.randn((B4, Hq, d_k), device="cuda").bfloat16()
+    table4, none = torch.full((B4, 4), -1, dtype=torch.int32, device="cuda"), torch.zeros(B4, dtype=torch.int32, device="cuda")
+    out4, out, qd, btd = torch.empty((B4, Hq, d_v), dtype=torch.bfloat16, device="cuda"), torch.empty_like(want), q.cuda(), torch.from_numpy(bt).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    size = max(bdfp4.bdfp4_decode_workspace_size(B4, Hq, d_v, 4, 1), bdfp8.workspace_for(2, 1, 8, 2, 128, bt.shape[1], 1).numel())
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        out4.fill_(1.0)
+        bdfp4.bdfp4_decode(q4, c4, table4, none, kv, 0.1, 1, ws, out4)
+        bdfp8.bdfp8_decode(qd, cache, btd, sl, 1 / math.sqrt(128), 1, ws, out)
+        assert torch.equal(out, want) and not out4.any()
+
+
 def test_a_given_stream_and_misaligned_views():
     lens = [300]
     cache, bt = make_cache(lens, 2, 128, bdfp8.E4M3, 32)
