@@ -23,6 +23,9 @@ DEV_BAD_POSITION = 16
 
 #: names of every entry point declared in include/bdfp8.h
 ENTRY_POINTS = ("bdfp8_append", "bdfp8_decode_plan", "bdfp8_decode_workspace_size", "bdfp8_decode")
+#: names of every entry point declared in include/bdfp8_debug.h (test hooks)
+DEBUG_ENTRY_POINTS = ("bdfp8_debug_decode_wait_test",)
+STALL_NONE, STALL_TILE, STALL_WARP = 0, 1, 2
 
 _lib = None
 _py = None
@@ -43,6 +46,9 @@ def load() -> ctypes.CDLL:
         L.bdfp8_decode_workspace_size.restype = sz
         L.bdfp8_decode.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i64, i, i, i, f, i, p, sz, p, p, p]
         L.bdfp8_decode.restype = i
+        L.bdfp8_debug_decode_wait_test.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i64, i, i, i, f, i, p, sz, p, p,
+                                                   ctypes.c_longlong, i, p]
+        L.bdfp8_debug_decode_wait_test.restype = i
         from . import _bdfp8_py
         _bdfp8_py.set_error(BDFP4Error)
         _lib, _py = L, _bdfp8_py
@@ -143,4 +149,22 @@ def bdfp8_decode(q: torch.Tensor, cache: FP8Cache, block_table: torch.Tensor, se
         seq_lens, sm_scale, chunk_tiles, workspace, out, window, sinks, dev_status, stream and stream.cuda_stream)
     if rc:
         bdfp4._check(rc, "bdfp8_decode")
+    return out
+
+
+def bdfp8_debug_decode_wait_test(q: torch.Tensor, cache: FP8Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                 sm_scale: float, chunk_tiles: int, workspace: torch.Tensor | None, out: torch.Tensor,
+                                 wait_limit_cycles: int, stall: int, window: int = 0, sinks: int = 0,
+                                 dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Test hook (include/bdfp8_debug.h): bdfp8_decode with a short in-kernel wait
+    bound and something (STALL_*) going wrong in every block."""
+    B, T_q, H_q, d = q.shape
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ptr = bdfp4._ptr
+    rc = load().bdfp8_debug_decode_wait_test(
+        ptr(q), ptr(cache.k_pages), ptr(cache.v_pages), ptr(cache.kv_scales), ptr(block_table), ptr(seq_lens), B, T_q,
+        H_q, cache.H_kv, d, block_table.shape[1], cache.num_pages, cache.fmt, window, sinks, float(sm_scale),
+        int(chunk_tiles), ptr(workspace), ws_bytes, ptr(out), ptr(dev_status), int(wait_limit_cycles), int(stall),
+        bdfp4._stream(stream))
+    bdfp4._check(rc, "bdfp8_debug_decode_wait_test")
     return out

@@ -122,10 +122,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int FMT, int D, int ROWS, bool MT>
+// HOOK: the unwind test's instantiation (bdfp8_debug.h).
+template <int FMT, int D, int ROWS, bool MT, bool HOOK>
 __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, ROWS, MT>::CTAS)
     decode_fp8_kernel(const Args a) {
     using C = Cfg<FMT, D, ROWS, MT>;
+    const long long wlim = HOOK ? a.wait_limit : kWaitLimit;
     constexpr int HG = C::HG;
     follow_grid();
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
     const uint32_t tbase = *tmem_slot;
 
     if (warp == C::PRODUCER) {
-        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
+        produce<C, HOOK>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             uint32_t last_par = 0;
             auto issue_qk = [&](int j) -> bool {
                 const int s = j % C::NSK, buf = j & 1;
-                if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, kWaitLimit)) return false;
+                if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, wlim)) return false;
                 tc::tc_fence_after();
                 const uint32_t kt = k_lo + s * (C::TILE / 16), d = tbase + C::T_S + buf * C::NQ;
                 mma_f8<false>(d, kt, qk_hi, q_lo, qk_hi, idesc_qk);
@@ -242,14 +244,14 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 last_par = (uint32_t)(j / C::NSK) & 1u;
                 return true;
             };
-            bool ok = tc::mbar_wait(q_ready, 0, abort_flag, kWaitLimit);
+            bool ok = tc::mbar_wait(q_ready, 0, abort_flag, wlim);
             if (ok) tc::tc_fence_after();
             ok = ok && issue_qk(0);
             for (int j = 0; ok && j < n; ++j) {
                 if (j + 1 < n && !(ok = issue_qk(j + 1))) break;
                 const int s = j % C::NSV, buf = j & 1;
-                if (!(ok = tc::mbar_wait(&p_ready[buf], (j >> 1) & 1, abort_flag, kWaitLimit))) break;
-                if (!(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit))) break;
+                if (!(ok = tc::mbar_wait(&p_ready[buf], (j >> 1) & 1, abort_flag, wlim))) break;
+                if (!(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim))) break;
                 tc::tc_fence_after();
                 const uint32_t vt = v_lo + s * (C::TILE / 16), pt = p_lo + buf * (C::P_BUF / 16), d = tbase + C::T_O;
                 // O^T accumulates over the split's tiles (the softmax warps rescale it)
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             if (!ok) {
                 *abort_flag = 1;
                 // the tensor memory is freed below: the MMAs into it must have finished
-                if (last_bar) tc::mbar_wait_drain(last_bar, last_par, kWaitLimit);
+                if (last_bar) tc::mbar_wait_drain(last_bar, last_par, wlim);
             }
         }
         __syncwarp();
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             // O^T of the group's rows moves to the new maximum (and scale bound) once the previous
             // tile's PV has completed, before this tile's PV is issued
             if (j > 0 && rose) {
-                if (!tc::mbar_wait(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+                if (!tc::mbar_wait(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim)) bad = true;
                 tc::tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             if (!full && grp == 0) {
                 const uint4 vm = *reinterpret_cast<const uint4*>(vmask + (buf * C::NSG + grp) * 4);
                 const int s = j % C::NSV;
-                if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit)) bad = true;
+                if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim)) bad = true;
                 const uint32_t w[4] = {vm.x, vm.y, vm.z, vm.w};
                 if (chan < D) {
                     uint8_t* const vc = smem + C::SM_V + s * C::TILE + (chan >> 3) * 512 + (chan & 7) * 16;
@@ -453,7 +455,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
 
         for (int j = 0; j < n; ++j) {
             const int t0 = tl.tile(tile0 + j) * kTileTokens;
-            if (!tc::mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+            if (!tc::mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag, wlim)) bad = true;
+            if (HOOK && a.stall == kStallWarp && j == 0 && warp == 0) bad = true;
             tc::tc_fence_after();
             const int good = pok[j % C::NSC];
             if (good == 3 && t0 + kTileTokens <= all_end && (t0 >= all_lo || t0 + kTileTokens <= a.sinks))
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         // ------------------------------------------------------------ epilogue (thread = channel)
         uint32_t o1[HG], o2[HG], o3[HG];
         if (!grp_abort) {
-            if (!tc::mbar_wait(&o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+            if (!tc::mbar_wait(&o_full[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, wlim)) bad = true;
             tc::tc_fence_after();
             tc::tmem_ld<HG>(t_o, o1);
             tc::tmem_ld<HG>(t_o + HG, o2);
@@ -636,16 +639,16 @@ static int launch_merge8(const Args& a, int rows_per_cta, cudaStream_t st) {
     return launch_status();
 }
 
-template <int FMT, int D, int ROWS, bool MT>
+template <int FMT, int D, int ROWS, bool MT, bool HOOK = false>
 static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
     using C = Cfg<FMT, D, ROWS, MT>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT>, C::SMEM, done);
+    cudaError_t e = allow_smem(decode_fp8_kernel<FMT, D, ROWS, MT, HOOK>, C::SMEM, done);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
     }
-    e = launch_following(decode_fp8_kernel<FMT, D, ROWS, MT>, (unsigned)ctas, C::THREADS, C::SMEM,
+    e = launch_following(decode_fp8_kernel<FMT, D, ROWS, MT, HOOK>, (unsigned)ctas, C::THREADS, C::SMEM,
                          a.cluster ? (unsigned)a.max_splits : 1u, st, a);
     if (e != cudaSuccess) {
         record_cuda_error(e);
@@ -658,6 +661,11 @@ static int launch(const Args& a, int64_t ctas, cudaStream_t st) {
 
 template <int FMT, int D>
 static int dispatch(const Args& a, int rows, int64_t ctas, cudaStream_t st) {
+    if (a.wait_limit != kWaitLimit || a.stall) {   // bdfp8_debug_decode_wait_test: E4M3, d = 128
+        if constexpr (FMT != BDFP8_E4M3 || D != 128) return BDFP4_ERR_UNSUPPORTED;
+        else if (rows == 8 && a.T_q == 1) return launch<FMT, D, 8, false, true>(a, ctas, st);
+        else if (rows != kWideRows) return BDFP4_ERR_UNSUPPORTED;
+    }
     if (rows == kWideRows) {
         const int rc = launch_wide(a, FMT, D, ctas, st);
         return rc != BDFP4_OK ? rc : launch_merge8<D>(a, kWideRows, st);
@@ -802,11 +810,11 @@ extern "C" size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv,
     return partial_bytes(rows, s.max_splits, d) + (size_t)rows * s.max_splits * 2 * sizeof(float);
 }
 
-extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pages, const float* kv_scales,
-                            const int32_t* block_table, const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv,
-                            int d, int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, int window, int sinks,
-                            float sm_scale, int chunk_tiles, void* workspace, size_t workspace_bytes, void* out,
-                            int32_t* dev_status, void* stream) {
+static int run_decode8(const void* q, const void* k_pages, const void* v_pages, const float* kv_scales,
+                       const int32_t* block_table, const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv, int d,
+                       int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, int window, int sinks, float sm_scale,
+                       int chunk_tiles, void* workspace, size_t workspace_bytes, void* out, int32_t* dev_status,
+                       void* stream, long long wait_limit, int stall) {
     int rc = check_shape(B, T_q, H_q, H_kv, d, window, sinks);
     if (rc != BDFP4_OK) return rc;
     if (max_pages_per_seq <= 0 || num_pages < 0 || (fmt != BDFP8_E4M3 && fmt != BDFP8_E5M2)) return BDFP4_ERR_ARG;
@@ -862,8 +870,33 @@ extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pa
     a.num_pages = num_pages;
     a.chunk_tiles = chunk_tiles;
     a.sm_scale = sm_scale;
+    a.wait_limit = wait_limit;
+    a.stall = stall;
     cudaStream_t st = (cudaStream_t)stream;
     if (fmt == BDFP8_E4M3)
         return d == 128 ? dispatch<BDFP8_E4M3, 128>(a, s.rows, ctas, st) : dispatch<BDFP8_E4M3, 64>(a, s.rows, ctas, st);
     return d == 128 ? dispatch<BDFP8_E5M2, 128>(a, s.rows, ctas, st) : dispatch<BDFP8_E5M2, 64>(a, s.rows, ctas, st);
+}
+
+extern "C" int bdfp8_decode(const void* q, const void* k_pages, const void* v_pages, const float* kv_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv,
+                            int d, int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, int window, int sinks,
+                            float sm_scale, int chunk_tiles, void* workspace, size_t workspace_bytes, void* out,
+                            int32_t* dev_status, void* stream) {
+    return run_decode8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, B, T_q, H_q, H_kv, d, max_pages_per_seq,
+                       num_pages, fmt, window, sinks, sm_scale, chunk_tiles, workspace, workspace_bytes, out, dev_status,
+                       stream, kWaitLimit, 0);
+}
+
+extern "C" int bdfp8_debug_decode_wait_test(const void* q, const void* k_pages, const void* v_pages,
+                                            const float* kv_scales, const int32_t* block_table,
+                                            const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv, int d,
+                                            int max_pages_per_seq, int64_t num_pages, bdfp8_fmt fmt, int window,
+                                            int sinks, float sm_scale, int chunk_tiles, void* workspace,
+                                            size_t workspace_bytes, void* out, int32_t* dev_status,
+                                            long long wait_limit_cycles, int stall, void* stream) {
+    if (wait_limit_cycles <= 0 || stall < 0 || stall > BDFP8_STALL_WARP) return BDFP4_ERR_ARG;
+    return run_decode8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, B, T_q, H_q, H_kv, d, max_pages_per_seq,
+                       num_pages, fmt, window, sinks, sm_scale, chunk_tiles, workspace, workspace_bytes, out, dev_status,
+                       stream, std::min(wait_limit_cycles, kWaitLimit - 1), stall);
 }

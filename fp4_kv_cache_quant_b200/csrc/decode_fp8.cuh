@@ -2,6 +2,7 @@
 // the tiles that a group of query rows sees, query terms and the producer warp.
 #pragma once
 
+#include "../../include/bdfp8_debug.h"
 #include "decode_common.cuh"
 #include "fp8_device.cuh"
 #include "host_common.h"
@@ -25,6 +26,9 @@ struct Args {
     int merge_rows;   // 1: the merge kernel takes a warp per output row, 0: a block
     int64_t num_pages;
     float sm_scale;
+    // the unwind test's instantiations (bdfp8_debug.h): the bound of every wait in clock cycles, and what goes wrong
+    long long wait_limit;
+    int stall;
 };
 
 // The tiles that rows r0 .. r1 of a KV head's stacked rows see (row r is query token r / G).
@@ -118,6 +122,10 @@ constexpr int kTopExp = 11;
 
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 
+// What the unwind test does to a block: its first key tile is never announced; or one softmax warp gives up on its
+// first tile, which the others see arrive.
+constexpr int kStallTile = BDFP8_STALL_TILE, kStallWarp = BDFP8_STALL_WARP;
+
 // The block's place in a grid of B x H_kv x max_splits x groups: row groups of one split stand next to each
 // other (they read the same tiles), then the splits.
 struct Place {
@@ -150,10 +158,12 @@ __device__ __forceinline__ void early_pages(const Args& a, const Place& p, int l
 // has completed, and the MMA lane issues QK of tile t only after p_ready of tile t - 2: when
 // tile k's keys are issued, the softmax is done with the scales of tile k - NSK - 2, and
 // with NSC >= NSK + 2 slot k % NSC is free.
-template <class C>
+// HOOK: the unwind test's instantiation.
+template <class C, bool HOOK>
 __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile0, int n, int b, int hk, int lane, uint8_t* smem,
                                         float* sc_ring, int* pok, uint64_t* kfull, uint64_t* kempty, uint64_t* vfull,
                                         uint64_t* vempty, volatile int* abort_flag, const int (&early)[2]) {
+    const long long wlim = HOOK ? a.wait_limit : kWaitLimit;
     bool ok = true;
     int pv0 = -1, pv1 = -1;
     int k_last = -1, v_last = -1;
@@ -176,10 +186,10 @@ __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile
         for (int kk = 0; kk < kmax; ++kk) {
             const int k = j0 + kk, v = k - 1;
             const int pk0 = __shfl_sync(0xffffffffu, pg_l[0], kk), pk1 = __shfl_sync(0xffffffffu, pg_l[1], kk);
-            if (k < n) {
+            if (k < n && !(HOOK && k == 0 && a.stall == kStallTile)) {
                 const int s = k % C::NSK;
                 if (lane == 0) {
-                    if (k >= C::NSK && !tc::mbar_wait(&kempty[s], ((k / C::NSK) - 1) & 1, abort_flag, kWaitLimit)) {
+                    if (k >= C::NSK && !tc::mbar_wait(&kempty[s], ((k / C::NSK) - 1) & 1, abort_flag, wlim)) {
                         ok = false;
                     } else {
                         pok[k % C::NSC] = (pk0 >= 0 ? 1 : 0) | (pk1 >= 0 ? 2 : 0);
@@ -205,7 +215,7 @@ __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile
             if (v >= 0) {
                 const int s = v % C::NSV;
                 if (lane == 0) {
-                    if (v >= C::NSV && !tc::mbar_wait(&vempty[s], ((v / C::NSV) - 1) & 1, abort_flag, kWaitLimit))
+                    if (v >= C::NSV && !tc::mbar_wait(&vempty[s], ((v / C::NSV) - 1) & 1, abort_flag, wlim))
                         ok = false;
                     else
                         tc::mbar_arrive_expect_tx(&vfull[s], ((pv0 >= 0) + (pv1 >= 0)) * C::PAGE);
@@ -227,15 +237,15 @@ __device__ __forceinline__ void produce(const Args& a, const Tiles& tl, int tile
     if ((!ok || *abort_flag) && lane == 0) {
         for (int s = 0; s < C::NSK; ++s)
             if (k_last >= s)
-                tc::mbar_wait_drain(&kfull[s], ((k_last - (k_last - s) % C::NSK) / C::NSK) & 1, kWaitLimit);
+                tc::mbar_wait_drain(&kfull[s], ((k_last - (k_last - s) % C::NSK) / C::NSK) & 1, wlim);
         for (int s = 0; s < C::NSV; ++s)
             if (v_last >= s)
-                tc::mbar_wait_drain(&vfull[s], ((v_last - (v_last - s) % C::NSV) / C::NSV) & 1, kWaitLimit);
+                tc::mbar_wait_drain(&vfull[s], ((v_last - (v_last - s) % C::NSV) / C::NSV) & 1, wlim);
     }
     __syncwarp();
 }
 
-// The kernel for more than eight stacked rows (decode_fp8_wide.cu); launches on `st`, returns a host status.
+// The kernel for more than 16 stacked rows (decode_fp8_wide.cu); launches on `st`, returns a host status.
 constexpr int kWideRows = 128;
 int launch_wide(const Args& a, int fmt, int d, int64_t ctas, cudaStream_t st);
 

@@ -102,9 +102,11 @@ __device__ __forceinline__ uint32_t seen_bits(int lo, int end, int window, int s
     return m;
 }
 
-template <int FMT, int D>
+// HOOK: the unwind test's instantiation (bdfp8_debug.h).
+template <int FMT, int D, bool HOOK>
 __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_kernel(const Args a) {
     using C = WideCfg<FMT, D>;
+    const long long wlim = HOOK ? a.wait_limit : kWaitLimit;
     follow_grid();
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_op = smem + C::SM_Q;
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
     const uint32_t tbase = *tmem_slot;
 
     if (warp == C::PRODUCER) {
-        produce<C>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
+        produce<C, HOOK>(a, tl, tile0, n, b, hk, lane, smem, sc_ring, pok, kfull, kempty, vfull, vempty, abort_flag, early);
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         // (a warp for each stream, issuing side by side, took 1810 ns a tile)
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             uint32_t last_par = 0;
             auto issue_qk = [&](int j) -> bool {
                 const int s = j % C::NSK, wg = j & 1;
-                if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, kWaitLimit)) return false;
+                if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, wlim)) return false;
                 tc::tc_fence_after();
                 const uint32_t kt = k_lo + s * (C::TILE / 16), d = tbase + C::T_S + wg * 128;
                 mma_f8<false>(d, q_lo, qk_hi, kt, qk_hi, idesc_qk);
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 last_par = (uint32_t)(j / C::NSK) & 1u;
                 return true;
             };
-            bool ok = tc::mbar_wait(q_ready, 0, abort_flag, kWaitLimit);
+            bool ok = tc::mbar_wait(q_ready, 0, abort_flag, wlim);
             if (ok) tc::tc_fence_after();
             ok = ok && issue_qk(0) && (n < 2 || issue_qk(1));
             for (int j = 0; ok && j < n; ++j) {
@@ -221,8 +223,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 // 32 tokens a step: both halves' first ones, while the softmax is at the second
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (!(ok = tc::mbar_wait(&p_ready[2 * wg + i], (j >> 1) & 1, abort_flag, kWaitLimit))) break;
-                    if (i == 0 && !(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit))) break;
+                    if (!(ok = tc::mbar_wait(&p_ready[2 * wg + i], (j >> 1) & 1, abort_flag, wlim))) break;
+                    if (i == 0 && !(ok = tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim))) break;
                     tc::tc_fence_after();
 #pragma unroll
                     for (int c = i; c < 4; c += 2) {
@@ -239,14 +241,14 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 last_par = (uint32_t)(j / C::NSV) & 1u;
                 if (j + 2 < n) {
                     // the stream's next logits overwrite the probabilities
-                    if (!(ok = tc::mbar_wait(&o_full[wg], (j >> 1) & 1, abort_flag, kWaitLimit))) break;
+                    if (!(ok = tc::mbar_wait(&o_full[wg], (j >> 1) & 1, abort_flag, wlim))) break;
                     ok = issue_qk(j + 2);
                 }
             }
             if (!ok) {
                 *abort_flag = 1;
                 // the tensor memory is freed below: the MMAs into it must have finished
-                if (last_bar) tc::mbar_wait_drain(last_bar, last_par, kWaitLimit);
+                if (last_bar) tc::mbar_wait_drain(last_bar, last_par, wlim);
             }
         }
         __syncwarp();
@@ -429,7 +431,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
 
         for (int j = wg; j < n; j += 2) {
             const int t0 = tl.tile(tile0 + j) * kTileTokens;
-            bad = !tc::mbar_wait(&s_full[wg], (j >> 1) & 1, abort_flag, kWaitLimit);
+            // (a warp that gives up stays until the stream's vote: the others may have seen the tile arrive)
+            bad = !tc::mbar_wait(&s_full[wg], (j >> 1) & 1, abort_flag, wlim) || (HOOK && a.stall == kStallWarp && j == 0 && warp == 0);
             tc::tc_fence_after();
             const int good = pok[j % C::NSC];
             const bool full = good == 3 && t0 + kTileTokens <= all_end && (t0 >= all_lo || t0 + kTileTokens <= a.sinks);
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             // among them), and 0 times NaN is NaN.  One channel per thread of the stream's first half.
             if (!full && half == 0) {
                 const int chan = tid & 127, s = j % C::NSV;
-                if (tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, kWaitLimit) && chan < D) {
+                if (tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim) && chan < D) {
                     uint8_t* const vc = smem + C::SM_V + s * C::TILE + (chan >> 3) * 512 + (chan & 7) * 16;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -456,10 +459,9 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 }
                 tc::fence_proxy_async_smem();
             }
-            if (bad) break;
             if (live) {
                 bad = full ? !tile(std::true_type{}, j, t0, good) : !tile(std::false_type{}, j, t0, good);
-            } else {
+            } else if (!bad) {
                 arrive(0);
                 arrive(1);
             }
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
         // ------------------------------------------------------------ joining the streams
         const int last = n - 1 - ((n - 1 - wg) & 1);   // this stream's last tile (-1: none)
         const bool some = last >= wg;
-        if (some && !bad && !tc::mbar_wait(&o_full[wg], (last >> 1) & 1, abort_flag, kWaitLimit)) bad = true;
+        if (some && !bad && !tc::mbar_wait(&o_full[wg], (last >> 1) & 1, abort_flag, wlim)) bad = true;
         tc::tc_fence_after();
         const float2 l = unpair(l2);
         if (half == 0) ml[(3 * wg) * C::ROWS + r] = m;
@@ -537,13 +539,13 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
     }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool HOOK = false>
 static int launch_w(const Args& a, int64_t ctas, cudaStream_t st) {
     using C = WideCfg<FMT, D>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(decode_fp8_wide_kernel<FMT, D>, C::SMEM, done);
+    cudaError_t e = allow_smem(decode_fp8_wide_kernel<FMT, D, HOOK>, C::SMEM, done);
     if (e == cudaSuccess)
-        e = launch_following(decode_fp8_wide_kernel<FMT, D>, (unsigned)ctas, C::THREADS, C::SMEM, 1, st, a);
+        e = launch_following(decode_fp8_wide_kernel<FMT, D, HOOK>, (unsigned)ctas, C::THREADS, C::SMEM, 1, st, a);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return BDFP4_ERR_CUDA;
@@ -552,6 +554,7 @@ static int launch_w(const Args& a, int64_t ctas, cudaStream_t st) {
 }
 
 int launch_wide(const Args& a, int fmt, int d, int64_t ctas, cudaStream_t st) {
+    if (a.wait_limit != kWaitLimit || a.stall) return launch_w<BDFP8_E4M3, 128, true>(a, ctas, st);
     if (fmt == BDFP8_E4M3)
         return d == 128 ? launch_w<BDFP8_E4M3, 128>(a, ctas, st) : launch_w<BDFP8_E4M3, 64>(a, ctas, st);
     return d == 128 ? launch_w<BDFP8_E5M2, 128>(a, ctas, st) : launch_w<BDFP8_E5M2, 64>(a, ctas, st);

@@ -148,3 +148,21 @@ def test_reference_layout_is_a_bijection():
     for d in (64, 128):
         for o in ref.offsets(d):
             assert np.array_equal(np.sort(o.reshape(-1)), np.arange(64 * d))
+
+
+def test_wait_test_hook(lib):
+    """include/bdfp8_debug.h: exports, constants, and what it refuses before a launch."""
+    hdr = open(os.path.join(ROOT, "include", "bdfp8_debug.h")).read()
+    names = re.findall(r"BDFP4_API\s+[\w\s\*]+?\b(bdfp8_\w+)\s*\(", hdr)
+    assert tuple(names) == bdfp8.DEBUG_ENTRY_POINTS and all(hasattr(lib, n) for n in names)
+    defs = dict(re.findall(r"#define (BDFP8_STALL_\w+) (\d+)", hdr))
+    assert [int(defs["BDFP8_STALL_" + n]) for n in ("NONE", "TILE", "WARP")] == [bdfp8.STALL_NONE, bdfp8.STALL_TILE,
+                                                                               bdfp8.STALL_WARP]
+
+    def call(limit=1 << 20, stall=1, **kw):
+        a = dict(q=A, kp=A, vp=A, sc=A, bt=A, sl=A, B=2, T=1, H_q=16, H_kv=2, d=128, mp=4, np=16, fmt=0, w=0, s=0,
+                 scale=0.1, chunk=2, ws=None, wb=0, out=A)
+        a.update(kw)
+        return lib.bdfp8_debug_decode_wait_test(*[a[k] for k in a], None, limit, stall, None)
+    assert call(limit=0) == -1 and call(stall=3) == -1 and call(stall=-1) == -1 and call(q=None) == -1
+    assert call(B=0) == 0
