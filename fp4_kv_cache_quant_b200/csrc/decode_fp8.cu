@@ -8,11 +8,11 @@
 //  - q = (q1 + q2 / 16) / 2^s: two E4M3 terms.  A bf16 element has 8 significant
 //    bits, an E4M3 term 4, and the rest after rounding to 4 bits fits 4 bits: exact
 //    for elements down to 2^-13 of the row's largest.
-//  - p c = (P1 + P2 + P3) 2^(ev-11): three E5M2 terms, cut from an fp16 one after another
+//  - p c = (P1 + P2 + P3) 2^(m-11): three E5M2 terms, cut from an fp16 one after another
 //    (e5m2_terms: relative error 2^-9, which is bf16's own on average), with a floor at
-//    2^-28 of the largest, so a sink with a hundred thousand faint tokens behind it keeps
-//    their mass.  (E4M3 terms would be finer, 2^-12, but end at 2^-22.)  2^ev bounds the
-//    value scales seen so far.
+//    2^-28 of the row's largest p c, so a sink with a hundred thousand faint tokens behind it
+//    keeps their mass.  (E4M3 terms would be finer, 2^-12, but end at 2^-22.)  2^m bounds
+//    the row's p c so far (decode_fp8.cuh).
 // The terms are stacked as columns of one MMA (N = 2 rows of q, 3 rows of P), S^T =
 // K q^T with M = 128 tokens and O^T = V^T P^T with M = 128 channels.
 //
@@ -94,9 +94,8 @@ struct Cfg {
     static constexpr int SM_P = SM_V + NSV * TILE;
     static constexpr int SM_Q = SM_P + 2 * P_BUF;
     static constexpr int SM_SC = SM_Q + NQ * D;                                // [NSC][2 pages][8] scales
-    static constexpr int RED_Q = ROWS + NSG;                                    // a quadrant's maxima: rows, scale of each group
-    static constexpr int SM_RED = SM_SC + NSC * 2 * kScalePage * 4;           // [2][4][RED_Q]
-    static constexpr int SM_VM = (SM_RED + 2 * 4 * RED_Q * 4 + 15) / 16 * 16;   // [2][NSG][4] masks of visible tokens
+    static constexpr int SM_RED = SM_SC + NSC * 2 * kScalePage * 4;           // [2][4][ROWS] a quadrant's maxima
+    static constexpr int SM_VM = (SM_RED + 2 * 4 * ROWS * 4 + 15) / 16 * 16;   // [2][NSG][4] masks of visible tokens
     static constexpr int SM_LSC = SM_VM + 2 * NSG * 16;                       // [ROWS] logit factors
     static constexpr int SM_ROWS = SM_LSC + ROWS * 4;                         // [ROWS] their rows in the output
     static constexpr int SM_POK = SM_ROWS + ROWS * 4;                         // [NSC] page flags
@@ -302,13 +301,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         if (lane == 0) tc::mbar_arrive(q_ready);
 
         // The reference of row gb + hl lives in lanes hl, hl + HG, ... of the group's warps; the warp takes a new one
-        // by shuffle.  ev: 2^ev bounds the value scales seen so far (alike in all threads).
+        // by shuffle.
         const int hl = lane % HG;
         float m_l = -INFINITY;
-        int ev = -110;
-        float l_part[HG], mz[HG];   // mz: the references, 0 where there is none yet
+        float l_part[HG], mz[HG];   // mz: the references (0 where there is none yet) less kLift
 #pragma unroll
-        for (int g = 0; g < HG; ++g) l_part[g] = mz[g] = 0.0f;
+        for (int g = 0; g < HG; ++g) {
+            l_part[g] = 0.0f;
+            mz[g] = -(float)kLift;
+        }
         const int pg = qd >> 1;                                // page of this thread's token in the tile
         const int blk = 2 * (qd & 1) + (lane >> 4);            // its scale block in the page
         const int tok = 32 * qd + lane;
@@ -340,58 +341,50 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 vis0 = min(max(d, 0), a.T_q) * a.G - gb;
                 if (a.window > 0 && t >= a.sinks) vis1 = min(max(d + a.window, 0), a.T_q) * a.G - gb;
             }
-            // the warp's visible tokens, and the larger of its two blocks' value scales that any of them has
-            const uint32_t seen = full ? 0xffffffffu : __ballot_sync(0xffffffffu, valid);
-            float vmx = (seen >> (lane & 16)) & 0xffffu ? fabsf(va) : 0.0f;
-            vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, 16));
+            const uint32_t seen = full ? 0xffffffffu : __ballot_sync(0xffffffffu, valid);   // the warp's visible tokens
+            float ve, v_down;
+            scale_parts(va, ve, v_down);
             tc::tmem_wait_ld();
-            float x[HG];
+            float x[HG];   // x + e
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
-                const float s = fmaf(__uint_as_float(s12[HG + g]), 0.0625f, __uint_as_float(s12[g])) * (ka * lr[g]);
+                const float s = fmaf(fmaf(__uint_as_float(s12[HG + g]), 0.0625f, __uint_as_float(s12[g])), ka * lr[g], ve);
                 const bool see = full || (valid && (!MT || (g >= vis0 && g < vis1)));
                 x[g] = see ? s : -INFINITY;
             }
             const float wm_l = rows_reduce<HG, false>(x, lane);   // row hl's maximum over the warp's tokens
-            float* const rw = red + (buf * 4 + qd) * C::RED_Q;
+            float* const rw = red + (buf * 4 + qd) * ROWS;
             if (lane < HG) rw[gb + lane] = wm_l;
-            if (lane == 0) {
-                rw[ROWS + grp] = vmx;
-                if constexpr (!full) vmask[(buf * C::NSG + grp) * 4 + qd] = seen;
+            if constexpr (!full) {
+                if (lane == 0) vmask[(buf * C::NSG + grp) * 4 + qd] = seen;
             }
             // one decision for the group's four warps, taken by the barrier itself
             if (tc::named_bar_or(bar_id, 128, bad)) return false;
-            const float* const rr = red + buf * 4 * C::RED_Q;
-            const float mt = fmaxf(fmaxf(rr[gb + hl], rr[C::RED_Q + gb + hl]),
-                                   fmaxf(rr[2 * C::RED_Q + gb + hl], rr[3 * C::RED_Q + gb + hl]));
-            const float vt = fmaxf(fmaxf(rr[ROWS + grp], rr[C::RED_Q + ROWS + grp]),
-                                   fmaxf(rr[2 * C::RED_Q + ROWS + grp], rr[3 * C::RED_Q + ROWS + grp]));
-            // the smallest exponent with |scale| <= 2^ev over what has been seen
-            const int en = max(ev, min((int)((__float_as_uint(vt) + 0x7fffffu) >> 23) - 127, 127));
+            const float* const rr = red + buf * 4 * ROWS;
+            const float mt = fmaxf(fmaxf(rr[gb + hl], rr[ROWS + gb + hl]),
+                                   fmaxf(rr[2 * ROWS + gb + hl], rr[3 * ROWS + gb + hl]));
             const bool rise = mt > m_l + kRise;
-            const bool rose = __any_sync(0xffffffffu, rise || en != ev);
-            float corr_l = 1.0f, down = 1.0f;
+            const bool rose = __any_sync(0xffffffffu, rise);
+            float corr_l = 1.0f;
             if (rose) {
-                corr_l = rise ? tc::ex2_approx(m_l - mt) : 1.0f;   // 0 before the first visible token
-                down = pow2i(max(ev - en, -126));
+                corr_l = rise ? ex2_down(m_l - mt) : 1.0f;   // 0 before the first visible token
                 m_l = rise ? mt : m_l;
-                ev = en;
 #pragma unroll
                 for (int g = 0; g < HG; ++g) {
                     l_part[g] *= __shfl_sync(0xffffffffu, corr_l, g);
                     const float m = __shfl_sync(0xffffffffu, m_l, g);
-                    mz[g] = m == -INFINITY ? 0.0f : m;
+                    mz[g] = (m == -INFINITY ? 0.0f : m) - (float)kLift;
                 }
             }
-            // value scale in units of 2^(ev - kTopExp); nothing of a token that no row sees goes in
-            const float vy = valid ? va * pow2i(-ev) * (float)(1 << kTopExp) : 0.0f;
+            // r in units of 2^-kTopExp; nothing of a token that no row sees goes in
+            const float vy = valid ? va * v_down * (float)(1 << kTopExp) : 0.0f;
             uint8_t* const pb = pslot + buf * C::P_BUF;
 #pragma unroll
             for (int g = 0; g < HG; g += 2) {
                 const float p0 = tc::ex2_approx(x[g] - mz[g]);
                 const float p1 = tc::ex2_approx(x[g + 1] - mz[g + 1]);
-                l_part[g] += p0;
-                l_part[g + 1] += p1;
+                l_part[g] = fmaf(p0, v_down, l_part[g]);
+                l_part[g + 1] = fmaf(p1, v_down, l_part[g + 1]);
                 float y0 = p0 * vy, y1 = p1 * vy;
                 if constexpr (MT && !full) {   // a token that another row sees, with a scale that is no number
                     y0 = x[g] == -INFINITY ? 0.0f : y0;
@@ -405,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                     pb[(k * HG + g + 1) * 16] = (uint8_t)(c[k] >> 24);
                 }
             }
-            // O^T of the group's rows moves to the new maximum (and scale bound) once the previous
+            // O^T of the group's rows moves to the new reference once the previous
             // tile's PV has completed, before this tile's PV is issued
             if (j > 0 && rose) {
                 if (!tc::mbar_wait(&o_full[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, wlim)) bad = true;
@@ -417,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int g = 0; g < HG; ++g)
-                        ov[g] = __float_as_uint(__uint_as_float(ov[g]) * (__shfl_sync(0xffffffffu, corr_l, g) * down));
+                        ov[g] = __float_as_uint(__uint_as_float(ov[g]) * __shfl_sync(0xffffffffu, corr_l, g));
                     tc::tmem_st_n<HG>(t_o + k * HG, ov);
                 }
                 tc::tmem_wait_st();
@@ -480,15 +473,15 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
         if (!grp_abort) {
             float* const rl = red;   // [4][RED_Q] partial sums (the maxima are no longer read)
             const float l_l = rows_reduce<HG, true>(l_part, lane);
-            if (lane < HG) rl[qd * C::RED_Q + gb + lane] = l_l;
+            if (lane < HG) rl[qd * ROWS + gb + lane] = l_l;
             tc::named_bar_sync(bar_id, 128);
-            const float unit = pow2i(max(ev - kTopExp, -126));
+            const float unit = pow2i(-kTopExp);
 #pragma unroll
             for (int g = 0; g < HG; ++g) {
                 const int r = gb + g;
                 const float m_g = __shfl_sync(0xffffffffu, m_l, g);
                 if (r >= nrows || chan >= D) continue;
-                const float l = (rl[r] + rl[C::RED_Q + r]) + (rl[2 * C::RED_Q + r] + rl[3 * C::RED_Q + r]);
+                const float l = (rl[r] + rl[ROWS + r]) + (rl[2 * ROWS + r] + rl[3 * ROWS + r]);
                 const float o = ((__uint_as_float(o3[g]) + __uint_as_float(o2[g])) + __uint_as_float(o1[g])) * unit;
                 const int64_t row = rows[r];
                 if (nspl == 1) {
@@ -532,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             float L = 0.0f, acc = 0.0f;
 #pragma unroll
             for (int s = 0; s < kMaxCluster; ++s) {
-                const float w = tc::ex2_approx(ml[s].x - M);
+                const float w = ex2_down(ml[s].x - M);
                 L = fmaf(ml[s].y, w, L);
                 acc = fmaf(o[s], w, acc);
             }

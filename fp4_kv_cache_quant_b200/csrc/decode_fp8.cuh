@@ -113,12 +113,33 @@ __device__ __forceinline__ void put_query(uint8_t* op, int row, int lane, uint32
     else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)codes;
 }
 
-// A row's reference for its probabilities follows its maximum only when that has risen by more than kRise (log2
-// units): rescaling O waits for the value product before, and exact maxima rise in four of ten tiles of a split of
-// 32 (four rows a thread).  A probability is then at most 2^kRise; its terms, below 2^15, are in units of
-// 2^-kTopExp, which puts their floor at 2^-28 of the reference.
+// What goes into the value product is p c, a probability times its value block's scale c = 2^e r, 1/2 < r <= 1: so a
+// row's reference m is the maximum over the tokens that it sees of x + e (x the logit in log2 units), and with w =
+// 2^(x + e - m) the product takes w r and the sum of probabilities w 2^-e, both in units of 2^m.  Every row has its own
+// bound, however scales differ, and tokens that it does not see have no part in it.  (One bound on the scales for all rows of
+// a block cost rows with small values their bits beside a large block that only others saw, or that had no weight.)
+// The reference follows its maximum only when that has risen by more than kRise: rescaling O waits for the value
+// product before, and exact maxima rise in four of ten tiles of a split of 32 (four rows a thread).  So w <= 2^kRise;
+// the terms of w r, below 2^15, are in units of 2^-kTopExp, which puts their floor at 2^-28 of the row's largest p c.
+// w is computed as 2^kLift w: the exponential flushes below 2^-126, and a token whose p c is that far below the
+// largest may still have the larger p.
 constexpr float kRise = 4.0f;
-constexpr int kTopExp = 11;
+constexpr int kTopExp = 11, kLift = 22;
+
+// e and 2^(-e - kLift) of a scale.  e >= -96, as sums of w 2^-e over 2^26 tokens have to stay finite (a scale below, 0
+// among them, gives r < 1/2); the other is down to 2^-149, which fp32 holds.  A scale that is no number gets finite
+// ones: its r is none.
+__device__ __forceinline__ void scale_parts(float c, float& e, float& down) {
+    const uint32_t u = min(max((__float_as_uint(c) + 0x7fffffu) >> 23, 127u - 96u), 254u);
+    e = __uint_as_float(0x4b000000u + u) - (8388608.0f + 127.0f);
+    down = __uint_as_float(max((254u - u) << 23, 0x400000u)) * (1.0f / (float)(1 << kLift));
+}
+
+// 2^x for x <= 0, down to fp32's smallest (references of very different scales meet).
+__device__ __forceinline__ float ex2_down(float x) {
+    const float h = tc::ex2_approx(0.5f * x);
+    return h * h;
+}
 
 constexpr long long kWaitLimit = 1LL << 32;   // clock cycles (about 2 s)
 

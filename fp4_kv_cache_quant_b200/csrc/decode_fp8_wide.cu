@@ -80,11 +80,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // Column, from its S on, of the terms of tokens 32 c .. 32 c + 31 (each half of the tokens within its own logits).
 __device__ __forceinline__ constexpr int p_col(int c) { return 64 * (c >> 1) + 24 * (c & 1); }
@@ -285,7 +280,6 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
         const int all_end = N - a.T_q + r0 / a.G + 1;
         const int all_lo = a.window > 0 ? N - a.T_q + (r0 + nrows - 1) / a.G - a.window + 1 : 0;
         float m = -INFINITY;
-        int ev = -110;
         uint64_t l2 = pair(0.0f, 0.0f);
         float* const my_max = mx + (2 * wg + half) * C::ROWS + r;
         const float* const other_max = mx + (2 * wg + 1 - half) * C::ROWS + r;
@@ -300,34 +294,23 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
         auto tile = [&](auto full_c, int j, int t0, int good) -> bool {
             constexpr bool full = decltype(full_c)::value;
             const float* const sc = sc_ring + (j % C::NSC) * 2 * kScalePage;   // of two pages: keys 0-3, values 4-7
-            float ks[4], vs[4], vmax;   // this half's blocks (its page); 0 for blocks that no row sees
+            float ks[4], vs[4];   // this half's blocks (its page); 0 for blocks that no row sees
             *reinterpret_cast<float4*>(ks) = *reinterpret_cast<const float4*>(sc + half * kScalePage);
             *reinterpret_cast<float4*>(vs) = *reinterpret_cast<const float4*>(sc + half * kScalePage + 4);
-            const float4 vo = *reinterpret_cast<const float4*>(sc + (1 - half) * kScalePage + 4);
             uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            if constexpr (full) {
-                vmax = fmaxf(fmaxf(fabsf(vo.x), fabsf(vo.y)), fmaxf(fabsf(vo.z), fabsf(vo.w)));
-            } else {
-                const float v4[4] = {vo.x, vo.y, vo.z, vo.w};
-                vmax = 0.0f;
+            if constexpr (!full) {
+                const bool page = (good >> half) & 1;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int base = t0 + 64 * half + 32 * c, base_o = t0 + 64 * (1 - half) + 32 * c;
-                    const bool page = (good >> half) & 1, page_o = (good >> (1 - half)) & 1;
+                    const int base = t0 + 64 * half + 32 * c;
                     see[c] = page ? seen_bits(lo_r, pos + 1, a.window, a.sinks, base) : 0u;
                     const uint32_t any = page ? seen_bits(tl.lo, tl.end, a.window, a.sinks, base) : 0u;
-                    const uint32_t any_o = page_o ? seen_bits(tl.lo, tl.end, a.window, a.sinks, base_o) : 0u;
                     if (!(any & 0xffffu)) ks[2 * c] = vs[2 * c] = 0.0f;
                     if (!(any >> 16)) ks[2 * c + 1] = vs[2 * c + 1] = 0.0f;
-                    if (any_o & 0xffffu) vmax = fmaxf(vmax, fabsf(v4[2 * c]));
-                    if (any_o >> 16) vmax = fmaxf(vmax, fabsf(v4[2 * c + 1]));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                vmax = fmaxf(vmax, fabsf(vs[i]));
-                ks[i] *= lr;
-            }
+            for (int i = 0; i < 4; ++i) ks[i] *= lr;
             auto hide = [&](int blk, uint32_t* x) {   // 16 logits of block blk
                 const uint32_t w = see[blk >> 1] >> (16 * (blk & 1));
 #pragma unroll
@@ -351,7 +334,9 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                     for (int i = 4; i < 16; ++i) v[i & 3] = fmaxf(v[i & 3], __uint_as_float(x[i]));
                     const float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                     // a block with nothing to see has no maximum, whatever its factor (0 among them)
-                    mt = fmaxf(mt, bm == -INFINITY ? bm : bm * ks[blk]);
+                    float ve, v_down;
+                    scale_parts(vs[blk], ve, v_down);
+                    mt = fmaxf(mt, bm == -INFINITY ? bm : fmaf(bm, ks[blk], ve));
                 }
             }
             *my_max = mt;
@@ -359,32 +344,27 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             mt = fmaxf(mt, *other_max);
             uint32_t s[2][16];
             tc::tmem_ld<16>(ts, s[0]);
-            // a new reference, where the maximum has left the old one or a value scale its bound
-            const int en = max(ev, min((int)((__float_as_uint(vmax) + 0x7fffffu) >> 23) - 127, 127));
+            // a new reference, where the maximum has left the old one
             const bool rise = mt > m + kRise;
-            if (__any_sync(0xffffffffu, rise || en != ev)) {
-                const float corr = rise ? tc::ex2_approx(m - mt) : 1.0f;   // 0 before the first visible token
+            if (__any_sync(0xffffffffu, rise)) {
+                const float corr = rise ? ex2_down(m - mt) : 1.0f;   // 0 before the first visible token
                 l2 = mul2(l2, pair(corr, corr));
                 if (j > 1) {   // the stream's previous PV completed before its logits here were computed
-                    const float f = corr * pow2i(max(ev - en, -126));
 #pragma unroll 1
                     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
                         uint32_t o[32];
                         tc::tmem_ld<32>(to + c, o);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
                         tc::tmem_st16(to + c, o);
                         tc::tmem_st16(to + c + 16, o + 16);
                     }
                     tc::tmem_wait_st();
                 }
                 m = rise ? mt : m;
-                ev = en;
             }
-            const float mz = m == -INFINITY ? 0.0f : m;
-            const uint64_t negm = pair(-mz, -mz);
-            const float vu = pow2i(-ev) * (float)(1 << kTopExp);   // value scales in units of 2^(ev - kTopExp)
+            const float mz = (m == -INFINITY ? 0.0f : m) - (float)kLift;
             tc::tmem_wait_ld();
             // probabilities times value scales as three E5M2 terms
 #pragma unroll
@@ -392,8 +372,10 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 uint32_t* const x = s[blk & 1];
                 if (blk < 3) tc::tmem_ld<16>(ts + 16 * (blk + 1), s[(blk + 1) & 1]);
                 if constexpr (!full) hide(blk, x);
-                const float vb = vs[blk] * vu;
-                const uint64_t k2 = pair(ks[blk], ks[blk]), v2 = pair(vb, vb);
+                float ve, v_down;
+                scale_parts(vs[blk], ve, v_down);
+                const float vb = vs[blk] * v_down * (float)(1 << kTopExp), ref = ve - mz;   // - m + kLift
+                const uint64_t k2 = pair(ks[blk], ks[blk]), v2 = pair(vb, vb), ref2 = pair(ref, ref), down2 = pair(v_down, v_down);
                 uint32_t w[3][4];
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -401,13 +383,13 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float x0 = __uint_as_float(x[i + 2 * e]), x1 = __uint_as_float(x[i + 2 * e + 1]);
-                        float2 z = unpair(fma2(pair(x0, x1), k2, negm));
+                        float2 z = unpair(fma2(pair(x0, x1), k2, ref2));
                         if constexpr (!full) {   // -inf times a factor of 0 is no number
                             z.x = x0 == -INFINITY ? x0 : z.x;
                             z.y = x1 == -INFINITY ? x1 : z.y;
                         }
                         const uint64_t p = pair(tc::ex2_approx(z.x), tc::ex2_approx(z.y));
-                        l2 = add2(l2, p);
+                        l2 = fma2(p, down2, l2);
                         float2 y = unpair(mul2(p, v2));
                         if constexpr (!full) {   // nor is 0 times a scale that is none
                             y.x = x0 == -INFINITY ? 0.0f : y.x;
@@ -482,9 +464,9 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             const float m_o = ml[3 * (1 - wg) * C::ROWS + r];
             const float M = fmaxf(m, m_o), Mz = M == -INFINITY ? 0.0f : M;
             const float m0 = wg == 0 ? m : m_o, m1 = wg == 0 ? m_o : m;
-            const float L = (ml[C::ROWS + r] + ml[2 * C::ROWS + r]) * tc::ex2_approx(m0 - Mz) +
-                            (ml[4 * C::ROWS + r] + ml[5 * C::ROWS + r]) * tc::ex2_approx(m1 - Mz);
-            const float f = some ? tc::ex2_approx(m - Mz) * pow2i(max(ev - kTopExp, -126)) : 0.0f;
+            const float L = (ml[C::ROWS + r] + ml[2 * C::ROWS + r]) * ex2_down(m0 - Mz) +
+                            (ml[4 * C::ROWS + r] + ml[5 * C::ROWS + r]) * ex2_down(m1 - Mz);
+            const float f = some ? ex2_down(m - Mz) * pow2i(-kTopExp) : 0.0f;
             float* const xch = reinterpret_cast<float*>(smem);   // [D][ROWS]
             constexpr int Q = D / 4;                             // channels that a warpgroup writes out
             const int keep = (2 * wg + half) * Q, give = (2 * (1 - wg) + half) * Q;

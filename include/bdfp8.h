@@ -132,9 +132,11 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * Arithmetic: a query row is split into two E4M3 terms, exact for a bf16 element
  * down to 2^-9 of the row's largest (2^-13 with up to 16 rows), to 2^-17 of the
  * largest below; logits, softmax and sums are fp32; a probability times its value
- * block's scale goes into the value product as three E5M2 terms (relative error 2^-9,
- * a floor of 2^-28 of the largest).  Up to 16 G T_q rows of a KV head take one
- * kernel, more another that works on 128 rows at a time.
+ * block's scale (rounded up to a power of two, 2^-96 at the least) goes into the value
+ * product as three E5M2 terms: relative error 2^-9, a floor of 2^-28 of the largest such
+ * product among the tokens of a split that the row sees.  (A token whose product is
+ * below 2^-148 of that one's leaves the sum of probabilities too.)  Up to 16 G T_q rows
+ * of a KV head take one kernel, more another that works on 128 rows at a time.
  *
  * An empty sequence and a row that sees no token give zeros; 0 < N_b < T_q also
  * sets BDFP4_DEV_BAD_SEQLEN (rows at negative indexes see nothing), N_b outside
