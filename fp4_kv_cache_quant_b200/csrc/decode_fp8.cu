@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
             uint32_t s12[2 * HG];
             tc::tmem_ld<2 * HG>(tq + C::T_S + buf * C::NQ + 2 * gb, s12);
             const float* sc = sc_ring + ((j % C::NSC) * 2 + pg) * kScalePage + blk;
-            const float ka = sc[0], va = sc[kBlocksPerPage];
+            const float ka = sc[0];
+            float va = sc[kBlocksPerPage];
             const int t = t0 + tok;
             const bool valid = full || (t < tl.end && (t >= tl.lo || t < a.sinks) && ((good >> pg) & 1));
             // several query tokens: row r sees t iff r / G >= t - (N - T_q) and, in a window, r / G < t + W - (N - T_q)
@@ -352,7 +353,26 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                 const bool see = full || (valid && (!MT || (g >= vis0 && g < vis1)));
                 x[g] = see ? s : -INFINITY;
             }
-            const float wm_l = rows_reduce<HG, false>(x, lane);   // row hl's maximum over the warp's tokens
+            float wm_l = rows_reduce<HG, false>(x, lane);   // row hl's maximum over the warp's tokens
+            // blocks of zeros (see kZeroScale): each half of the warp looks at its tokens' block
+            if (__any_sync(0xffffffffu, valid && va == kZeroScale) && __any_sync(0xffffffffu, wm_l > m_l + kRise)) {
+                const int s = j % C::NSV;
+                if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim)) bad = true;
+                const uint8_t* const vb = smem + C::SM_V + s * C::TILE + pg * C::PAGE + blk * 128;
+                bool some = false;
+#pragma unroll 1
+                for (int c = lane & 15; c < D; c += 16)
+                    some |= any_value(*reinterpret_cast<const uint4*>(vb + (c >> 3) * 512 + (c & 7) * 16), seen >> (lane & 16));
+                some = (__ballot_sync(0xffffffffu, some) >> (lane & 16)) & 0xffffu;
+                if (va == kZeroScale && !some) {
+                    const float one = ve;
+                    va = 0.0f;
+                    scale_parts(va, ve, v_down);
+#pragma unroll
+                    for (int g = 0; g < HG; ++g) x[g] += ve - one;
+                }
+                wm_l = rows_reduce<HG, false>(x, lane);
+            }
             float* const rw = red + (buf * 4 + qd) * ROWS;
             if (lane < HG) rw[gb + lane] = wm_l;
             if constexpr (!full) {
@@ -429,12 +449,11 @@ __global__ void __launch_bounds__(Cfg<FMT, D, ROWS, MT>::THREADS, Cfg<FMT, D, RO
                         const uint32_t m = (w[c >> 1] >> (16 * (c & 1))) & 0xffffu;
                         if (m == 0xffffu) continue;
                         uint4* const at = reinterpret_cast<uint4*>(vc + (c >> 2) * C::PAGE + (c & 3) * 128);
-                        auto bytes = [](uint32_t m4) { return (((m4 & 15u) * 0x00204081u) & 0x01010101u) * 0xffu; };
                         uint4 v = *at;
-                        v.x &= bytes(m);
-                        v.y &= bytes(m >> 4);
-                        v.z &= bytes(m >> 8);
-                        v.w &= bytes(m >> 12);
+                        v.x &= byte_mask(m);
+                        v.y &= byte_mask(m >> 4);
+                        v.z &= byte_mask(m >> 8);
+                        v.w &= byte_mask(m >> 12);
                         *at = v;
                     }
                 }

@@ -135,6 +135,21 @@ __device__ __forceinline__ void scale_parts(float c, float& e, float& down) {
     down = __uint_as_float(max((254u - u) << 23, 0x400000u)) * (1.0f / (float)(1 << kLift));
 }
 
+// bdfp8_append gives a block of zeros scale 1, which says nothing of its values (those around it may have scales of
+// 2^-20) and must not become a reference: before a block of scale 1 moves one, its codes are looked at, and where all of
+// those that some row sees are zeros it counts as a block of scale 0.  That is rare (blocks of zeros beside others of scale
+// 1 or more move nothing), so tiles pay for a comparison only.
+constexpr float kZeroScale = 1.0f;
+
+// The bytes of four slots (bits 0-3 of m4) as a mask.
+__device__ __forceinline__ uint32_t byte_mask(uint32_t m4) { return (((m4 & 15u) * 0x00204081u) & 0x01010101u) * 0xffu; }
+
+// Whether any of 16 value codes of a channel (those in the mask) is not a zero of either sign.
+__device__ __forceinline__ bool any_value(const uint4& v, uint32_t mask16) {
+    return ((v.x & byte_mask(mask16)) | (v.y & byte_mask(mask16 >> 4)) | (v.z & byte_mask(mask16 >> 8)) |
+            (v.w & byte_mask(mask16 >> 12))) & 0x7f7f7f7fu;
+}
+
 // 2^x for x <= 0, down to fp32's smallest (references of very different scales meet).
 __device__ __forceinline__ float ex2_down(float x) {
     const float h = tc::ex2_approx(0.5f * x);

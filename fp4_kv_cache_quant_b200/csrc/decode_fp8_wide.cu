@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 for (int i = 0; i < 16; ++i) x[i] = (w >> i) & 1 ? x[i] : 0xff800000u;
             };
             // the row's maximum over this half, then over both
-            float mt = -INFINITY;
+            float bm[4];   // a block's largest logit
             {
                 uint32_t s[2][32];
                 tc::tmem_ld<32>(ts, s[0]);
@@ -332,12 +332,38 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(x[i]);
 #pragma unroll
                     for (int i = 4; i < 16; ++i) v[i & 3] = fmaxf(v[i & 3], __uint_as_float(x[i]));
-                    const float bm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                    bm[blk] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                }
+            }
+            auto maximum = [&] {
+                float t = -INFINITY;
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
                     // a block with nothing to see has no maximum, whatever its factor (0 among them)
                     float ve, v_down;
                     scale_parts(vs[blk], ve, v_down);
-                    mt = fmaxf(mt, bm == -INFINITY ? bm : fmaf(bm, ks[blk], ve));
+                    t = fmaxf(t, bm[blk] == -INFINITY ? bm[blk] : fmaf(bm[blk], ks[blk], ve));
                 }
+                return t;
+            };
+            float mt = maximum();
+            // blocks of zeros (see kZeroScale), each warp for its own rows
+            if ((vs[0] == kZeroScale || vs[1] == kZeroScale || vs[2] == kZeroScale || vs[3] == kZeroScale) &&
+                __any_sync(0xffffffffu, mt > m + kRise)) {
+                const int s = j % C::NSV;
+                if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim)) bad = true;
+                const uint8_t* const vb = smem + C::SM_V + s * C::TILE + half * C::PAGE;
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    if (vs[blk] != kZeroScale) continue;
+                    const uint32_t any = full ? 0xffffu : seen_bits(tl.lo, tl.end, a.window, a.sinks, t0 + 64 * half + 32 * (blk >> 1)) >> (16 * (blk & 1));
+                    bool some = false;
+#pragma unroll 1
+                    for (int c = lane; c < D; c += 32)
+                        some |= any_value(*reinterpret_cast<const uint4*>(vb + (c >> 3) * 512 + blk * 128 + (c & 7) * 16), any);
+                    if (!__any_sync(0xffffffffu, some)) vs[blk] = 0.0f;
+                }
+                mt = maximum();
             }
             *my_max = mt;
             if (tc::named_bar_or(2 + wg, live_threads, bad)) return false;
@@ -430,12 +456,11 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                         const uint32_t mk = (word >> (16 * (c & 1))) & 0xffffu;
                         if (mk == 0xffffu) continue;
                         uint4* const at = reinterpret_cast<uint4*>(vc + (c >> 2) * C::PAGE + (c & 3) * 128);
-                        auto bytes = [](uint32_t m4) { return (((m4 & 15u) * 0x00204081u) & 0x01010101u) * 0xffu; };
                         uint4 v = *at;
-                        v.x &= bytes(mk);
-                        v.y &= bytes(mk >> 4);
-                        v.z &= bytes(mk >> 8);
-                        v.w &= bytes(mk >> 12);
+                        v.x &= byte_mask(mk);
+                        v.y &= byte_mask(mk >> 4);
+                        v.z &= byte_mask(mk >> 8);
+                        v.w &= byte_mask(mk >> 12);
                         *at = v;
                     }
                 }

@@ -135,7 +135,9 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * block's scale (rounded up to a power of two, 2^-96 at the least) goes into the value
  * product as three E5M2 terms: relative error 2^-9, a floor of 2^-28 of the largest such
  * product among the tokens of a split that the row sees.  (A token whose product is
- * below 2^-148 of that one's leaves the sum of probabilities too.)  Up to 16 G T_q rows
+ * below 2^-148 of that one's leaves the sum of probabilities too.)  A value block of
+ * scale 1 whose codes in tokens that a row sees are all zeros, as bdfp8_append leaves a
+ * block of zeros, counts as one of scale 0 in this.  Up to 16 G T_q rows
  * of a KV head take one kernel, more another that works on 128 rows at a time.
  *
  * An empty sequence and a row that sees no token give zeros; 0 < N_b < T_q also

@@ -24,7 +24,7 @@ def check(out, q, cache, bt, lens, window=0, sinks=0):
       4 ln 2 2^-24 (3 (X + E) + 44)   exponents x + e: three roundings (the sum, the reference, their difference), and of the
                                       22 that they are lifted by; in p and in the sum of p
       2^-19                           exponentials (2 units of 2^-22 each, twice where references meet) and the last product
-    and by n 2^-28 max_t p_t 2^e max_t |code|: the terms' floor."""
+    and by n 2^-28 max_t p_t 2^e max_t |code|: the terms' floor.  Blocks whose seen values are all zero have no part in it."""
     K, V = ref.values_of(cache)
     x, d, H = q.double().numpy(), q.shape[3], cache.H_kv
     G, T = q.shape[2] // H, q.shape[1]
@@ -50,7 +50,8 @@ def check(out, q, cache, bt, lens, window=0, sinks=0):
                 far = 3 * (np.abs(lg).max(1) / math.log(2) + np.abs(e2).max()) + 44
                 rel = (2.0 ** -9 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -23 * D + 2.0 ** -16 * left + (n + 64) * 2.0 ** -23 +
                        4 * math.log(2) * 2.0 ** -24 * far + 2.0 ** -19)
-                floor = n * 2.0 ** -28 * (e * 2.0 ** e2).max(1) * np.abs(v / np.maximum(ct, 2.0 ** -140)[:, None]).max()
+                used = np.isin(t // 16, np.unique(t[v.any(1)] // 16))
+                floor = n * 2.0 ** -28 * (e * np.where(used, 2.0 ** e2, 0)).max(1) * np.abs(v / np.maximum(ct, 2.0 ** -140)[:, None]).max()
                 lim = 2.0 ** -8 * np.abs(want) + A * rel[:, None] + floor[:, None]
                 off = np.abs(got[b, i, h * G: (h + 1) * G] - want) - lim
                 assert np.all(off <= 0), (b, i, h, float((off / np.maximum(A, 1e-300)).max()))
@@ -135,3 +136,92 @@ def test_the_smallest_scales(low, G):
     q = queries(2, 1, 2 * G, 128, 69)
     for chunk in (1, 3):
         check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
+
+
+# ------------------------------------------------------------------------------------------------ blocks of zeros
+def appended(lens, H, d, fmt, std, zeros, toward, seed):
+    """A cache written by bdfp8_append, values N(0, std) but zeros (of both signs) in the token ranges zeros[b], whose keys lie
+    along element 0 when `toward`; whatever no append wrote holds NaN codes and scales."""
+    g = torch.Generator().manual_seed(seed)
+    mp = max((n + 63) // 64 for n in lens)
+    P = len(lens) * mp + 1
+    bt = torch.randperm(P, generator=g)[: len(lens) * mp].view(len(lens), mp).int()
+    cache = bdfp8.FP8Cache.empty(P, H, d, fmt)
+    cache.k_pages.fill_(0x7F)
+    cache.v_pages.fill_(0x7F)
+    cache.kv_scales.fill_(float("nan"))
+    ks, vs = [], []
+    for n, zs in zip(lens, zeros):
+        k, v = torch.randn((n, H, d), generator=g), torch.randn((n, H, d), generator=g) * std
+        for a, e in zs:
+            v[a:e] *= 0.0
+            if toward:
+                k[a:e] = 0.0
+                k[a:e, :, 0] = 8.0
+        ks.append(k)
+        vs.append(v)
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).int().cuda()
+    bdfp8.bdfp8_append(torch.cat(ks).bfloat16().cuda(), torch.cat(vs).bfloat16().cuda(), cu,
+                       torch.tensor(lens, dtype=torch.int32).cuda(), bt.cuda(), None, cache, bdfp8.OpenBlocks.empty(len(lens), H, d))
+    return cache, bt.numpy()
+
+
+@pytest.mark.parametrize("toward", [False, True])
+@pytest.mark.parametrize("std", [0.1, 0.01, 0.001])
+@pytest.mark.parametrize("d, fmt", FORMS)
+@pytest.mark.parametrize("T, G", [(1, 4), (1, 8), (1, 16), (1, 24), (3, 2), (3, 40)])
+def test_a_block_of_zero_values_among_small_ones(T, G, d, fmt, std, toward):
+    """A whole block of zeros, with and without most of the weight, and an open one."""
+    lens = [700, 146]
+    cache, bt = appended(lens, 2, d, fmt, std, [[(48, 64), (300, 310)], [(0, 16), (144, 146)]], toward, 70)
+    assert float(cache.kv_scales[int(bt[0, 0]), 0, 1, 3]) == 1.0
+    q = queries(2, T, 2 * G, d, 71)
+    if toward:
+        q[..., 0] = q[..., 0].abs() + 4.0
+    for chunk in (1, 6):
+        check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)
+
+
+@pytest.mark.parametrize("G", [4, 8, 16, 24])
+def test_zeros_in_every_seen_slot(G):
+    """Junk behind the sequence's end, and a block whose other tokens are behind the window."""
+    lens, window = [133, 133], 101    # the window begins at token 32; the last block holds tokens 128 .. 132
+    cache, bt = make_cache(lens, 2, 128, bdfp8.E5M2, 72, window)
+    cache.kv_scales[:, :, 1] *= 2.0 ** -20
+    _, vo = ref.offsets(128)
+    pages = cache.v_pages.cpu().numpy()
+    for pg, slots, blk in ((bt[0, 2], slice(0, 5), 0), (bt[1, 0], slice(33, 48), 2)):
+        for h in range(2):
+            pages[pg, h][vo[slots]] = 0x80
+        cache.kv_scales[int(pg), :, 1, blk] = 1.0
+    for h in range(2):
+        pages[bt[1, 0], h][vo[32]] = 0
+    cache.v_pages.copy_(torch.from_numpy(pages))
+    q = queries(2, 1, 2 * G, 128, 73)
+    for chunk in (1, 2):
+        check(decode(q, cache, bt, lens, chunk, window), q, cache, bt, lens, window)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [4, 8, 16, 24])
+@pytest.mark.parametrize("slot, chan", [(0, 0), (15, -1), (7, 8), (8, 31), (31, 5)])
+def test_one_value_makes_a_block_of_scale_one_count(slot, chan, G, d):
+    cache, bt = make_cache([200], 1, d, bdfp8.E4M3, 74)
+    cache.kv_scales[:, :, 1] *= 2.0 ** -20
+    _, vo = ref.offsets(d)
+    pages = cache.v_pages.cpu().numpy()
+    for page, base in ((0, 0), (1, 32)):
+        pages[bt[0, page], 0][vo[base: base + 32]] = 0
+        pages[bt[0, page], 0][vo[base + slot, chan]] = 0xC0   # -2
+        cache.kv_scales[int(bt[0, page]), 0, 1, base // 16: base // 16 + 2] = 1.0
+    cache.v_pages.copy_(torch.from_numpy(pages))
+    q = queries(1, 1, G, d, 75)
+    for chunk in (1, 2):
+        check(decode(q, cache, bt, [200], chunk), q, cache, bt, [200])
+
+
+@pytest.mark.parametrize("G", [4, 24])
+def test_nothing_but_zeros(G):
+    cache, bt = appended([300], 1, 128, bdfp8.E4M3, 1.0, [[(0, 300)]], False, 76)
+    got = decode(queries(1, 2, G, 128, 77), cache, bt, [300], 1)
+    assert not got.any()
