@@ -46,12 +46,13 @@ struct WideCfg {
     static constexpr int SM_LSC = SM_SC + NSC * 2 * kScalePage * 4;   // [ROWS] logit factors
     static constexpr int SM_MAX = SM_LSC + ROWS * 4;                  // [2][2][ROWS] a tile's maxima, by stream and half
     static constexpr int SM_ML = SM_MAX + 4 * ROWS * 4;               // [2][3][ROWS] a stream's maxima and its halves' sums
-    static constexpr int SM_POK = SM_ML + 6 * ROWS * 4;               // [NSC] page flags
+    static constexpr int SM_PART = SM_ML + 6 * ROWS * 4;              // [NSW][4][4] a warp's factors of its four blocks
+    static constexpr int SM_POK = SM_PART + NSW * 64;                 // [NSC] page flags
     static constexpr int SM_BARS = SM_POK + NSC * 4;
-    static constexpr int NBARS = 2 * NSK + 2 * NSV + 9;
+    static constexpr int NBARS = 2 * NSK + 2 * NSV + 11;
     static constexpr int SM_MISC = SM_BARS + NBARS * 8;
     static constexpr int SMEM = SM_MISC + 16;
-    static_assert(SM_BARS % 8 == 0 && SMEM <= 232448, "shared memory");
+    static_assert(SM_PART % 16 == 0 && SM_BARS % 8 == 0 && SMEM <= 232448, "shared memory");
     static_assert(NSC >= NSK + 3, "scale slots: the streams' tiles finish a tile apart");
     // at the end the rings hold each stream's half of O for the other
     static_assert(ROWS * D * 4 <= SM_Q, "exchange buffer");
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
     uint64_t* const kempty = kfull + C::NSK;
     uint64_t* const vfull = kempty + C::NSK;
     uint64_t* const vempty = vfull + C::NSV;
-    uint64_t* const s_full = vempty + C::NSV;   // [2] QK done, and the tile's scales seen -> softmax
+    uint64_t* const k_seen = vempty + C::NSV;   // [2] the tile's keys, scales and page flags are there -> softmax
+    uint64_t* const s_full = k_seen + 2;        // [2] QK done -> softmax
     uint64_t* const p_ready = s_full + 2;       // [2][2] a half's first, second 32 tokens of P written -> MMA
     uint64_t* const o_full = p_ready + 4;       // [2] PV done -> MMA lane, epilogue
     uint64_t* const q_ready = o_full + 2;
@@ -156,7 +158,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             tc::mbar_init(&vempty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&s_full[i], 2);   // the MMAs' commit, and the MMA lane itself
+            tc::mbar_init(&k_seen[i], 1);
+            tc::mbar_init(&s_full[i], 1);
             tc::mbar_init(&p_ready[2 * i], C::NSW / 2);
             tc::mbar_init(&p_ready[2 * i + 1], C::NSW / 2);
             tc::mbar_init(&o_full[i], 1);
@@ -194,6 +197,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             auto issue_qk = [&](int j) -> bool {
                 const int s = j % C::NSK, wg = j & 1;
                 if (!tc::mbar_wait(&kfull[s], (j / C::NSK) & 1, abort_flag, wlim)) return false;
+                // passes on this thread's view of the copied scales and the page flags
+                tc::mbar_arrive(&k_seen[wg]);
                 tc::tc_fence_after();
                 const uint32_t kt = k_lo + s * (C::TILE / 16), d = tbase + C::T_S + wg * 128;
                 mma_f8<false>(d, q_lo, qk_hi, kt, qk_hi, idesc_qk);
@@ -203,8 +208,6 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                                  idesc_qk);
                 tc::mma_commit(&s_full[wg]);
                 tc::mma_commit(&kempty[s]);
-                // passes on this thread's view of the copied scales and the page flags
-                tc::mbar_arrive(&s_full[wg]);
                 last_bar = &kempty[s];
                 last_par = (uint32_t)(j / C::NSK) & 1u;
                 return true;
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
         const int all_lo = a.window > 0 ? N - a.T_q + (r0 + nrows - 1) / a.G - a.window + 1 : 0;
         float m = -INFINITY;
         uint64_t l2 = pair(0.0f, 0.0f);
+        float4* const my_part = reinterpret_cast<float4*>(smem + C::SM_PART) + warp * 4;
         float* const my_max = mx + (2 * wg + half) * C::ROWS + r;
         const float* const other_max = mx + (2 * wg + 1 - half) * C::ROWS + r;
 
@@ -289,28 +293,31 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&p_ready[2 * wg + i]);
         };
+        // What the rows need of this half's four blocks in a tile is worked out once for the warp, block lane % 4 in each
+        // lane, while its logits are still being computed (per row, behind them, it cost 10 % at 32 rows): the key scale, e and
+        // 2^(-e - kLift) of the value scale, r in units of 2^(-kTopExp - kLift); blocks that no row sees get those of scales
+        // of 0.  Returns the blocks whose value scale is kZeroScale.
+        auto put_part = [&](int j, int t0, int good, bool full) -> uint32_t {
+            const float* const sc = sc_ring + ((j % C::NSC) * 2 + half) * kScalePage;   // the half's page: keys 0-3, values 4-7
+            float k = sc[lane & 3], v = sc[kBlocksPerPage + (lane & 3)];
+            if (!full && !((good >> half) & 1 && seen_bits(tl.lo, tl.end, a.window, a.sinks, t0 + 64 * half + 16 * (lane & 3)) & 0xffffu))
+                k = v = 0.0f;
+            float ve, v_down;
+            scale_parts(v, ve, v_down);
+            if (lane < 4) my_part[lane] = make_float4(k, ve, v_down, v * v_down * (float)(1 << kTopExp));
+            __syncwarp();
+            return __ballot_sync(0xffffffffu, v == kZeroScale) & 15u;
+        };
         // One tile's logits to probabilities, this half's 64 tokens; FULL: every row sees every token of the tile.
         // False: a warp of the stream gave up.
-        auto tile = [&](auto full_c, int j, int t0, int good) -> bool {
+        auto tile = [&](auto full_c, int j, int t0, int good, uint32_t zeros) -> bool {
             constexpr bool full = decltype(full_c)::value;
-            const float* const sc = sc_ring + (j % C::NSC) * 2 * kScalePage;   // of two pages: keys 0-3, values 4-7
-            float ks[4], vs[4];   // this half's blocks (its page); 0 for blocks that no row sees
-            *reinterpret_cast<float4*>(ks) = *reinterpret_cast<const float4*>(sc + half * kScalePage);
-            *reinterpret_cast<float4*>(vs) = *reinterpret_cast<const float4*>(sc + half * kScalePage + 4);
             uint32_t see[2] = {0xffffffffu, 0xffffffffu};
             if constexpr (!full) {
                 const bool page = (good >> half) & 1;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int base = t0 + 64 * half + 32 * c;
-                    see[c] = page ? seen_bits(lo_r, pos + 1, a.window, a.sinks, base) : 0u;
-                    const uint32_t any = page ? seen_bits(tl.lo, tl.end, a.window, a.sinks, base) : 0u;
-                    if (!(any & 0xffffu)) ks[2 * c] = vs[2 * c] = 0.0f;
-                    if (!(any >> 16)) ks[2 * c + 1] = vs[2 * c + 1] = 0.0f;
-                }
+                for (int c = 0; c < 2; ++c) see[c] = page ? seen_bits(lo_r, pos + 1, a.window, a.sinks, t0 + 64 * half + 32 * c) : 0u;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ks[i] *= lr;
             auto hide = [&](int blk, uint32_t* x) {   // 16 logits of block blk
                 const uint32_t w = see[blk >> 1] >> (16 * (blk & 1));
 #pragma unroll
@@ -340,34 +347,38 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
 #pragma unroll
                 for (int blk = 0; blk < 4; ++blk) {
                     // a block with nothing to see has no maximum, whatever its factor (0 among them)
-                    float ve, v_down;
-                    scale_parts(vs[blk], ve, v_down);
-                    t = fmaxf(t, bm[blk] == -INFINITY ? bm[blk] : fmaf(bm[blk], ks[blk], ve));
+                    const float2 f = *reinterpret_cast<const float2*>(my_part + blk);
+                    t = fmaxf(t, bm[blk] == -INFINITY ? bm[blk] : fmaf(bm[blk], f.x * lr, f.y));
                 }
                 return t;
             };
             float mt = maximum();
             // blocks of zeros (see kZeroScale), each warp for its own rows
-            if ((vs[0] == kZeroScale || vs[1] == kZeroScale || vs[2] == kZeroScale || vs[3] == kZeroScale) &&
-                __any_sync(0xffffffffu, mt > m + kRise)) {
+            if (zeros && __any_sync(0xffffffffu, mt > m + kRise)) {
                 const int s = j % C::NSV;
                 if (!tc::mbar_wait(&vfull[s], (j / C::NSV) & 1, abort_flag, wlim)) bad = true;
                 const uint8_t* const vb = smem + C::SM_V + s * C::TILE + half * C::PAGE;
-#pragma unroll
+#pragma unroll 1
                 for (int blk = 0; blk < 4; ++blk) {
-                    if (vs[blk] != kZeroScale) continue;
-                    const uint32_t any = full ? 0xffffu : seen_bits(tl.lo, tl.end, a.window, a.sinks, t0 + 64 * half + 32 * (blk >> 1)) >> (16 * (blk & 1));
+                    if (!((zeros >> blk) & 1)) continue;
+                    const uint32_t any = full ? 0xffffu : seen_bits(tl.lo, tl.end, a.window, a.sinks, t0 + 64 * half + 16 * blk);
                     bool some = false;
 #pragma unroll 1
                     for (int c = lane; c < D; c += 32)
                         some |= any_value(*reinterpret_cast<const uint4*>(vb + (c >> 3) * 512 + blk * 128 + (c & 7) * 16), any);
-                    if (!__any_sync(0xffffffffu, some)) vs[blk] = 0.0f;
+                    if (!__any_sync(0xffffffffu, some) && lane == 0) {
+                        float ve, v_down;
+                        scale_parts(0.0f, ve, v_down);
+                        my_part[blk] = make_float4(my_part[blk].x, ve, v_down, 0.0f);
+                    }
                 }
+                __syncwarp();
                 mt = maximum();
             }
             *my_max = mt;
             if (tc::named_bar_or(2 + wg, live_threads, bad)) return false;
             mt = fmaxf(mt, *other_max);
+            float4 fn = my_part[0];
             uint32_t s[2][16];
             tc::tmem_ld<16>(ts, s[0]);
             // a new reference, where the maximum has left the old one
@@ -398,10 +409,10 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 uint32_t* const x = s[blk & 1];
                 if (blk < 3) tc::tmem_ld<16>(ts + 16 * (blk + 1), s[(blk + 1) & 1]);
                 if constexpr (!full) hide(blk, x);
-                float ve, v_down;
-                scale_parts(vs[blk], ve, v_down);
-                const float vb = vs[blk] * v_down * (float)(1 << kTopExp), ref = ve - mz;   // - m + kLift
-                const uint64_t k2 = pair(ks[blk], ks[blk]), v2 = pair(vb, vb), ref2 = pair(ref, ref), down2 = pair(v_down, v_down);
+                const float4 f = fn;
+                if (blk < 3) fn = my_part[blk + 1];
+                const float kf = f.x * lr, ref = f.y - mz;   // e - m + kLift
+                const uint64_t k2 = pair(kf, kf), v2 = pair(f.w, f.w), ref2 = pair(ref, ref), down2 = pair(f.z, f.z);
                 uint32_t w[3][4];
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -440,10 +451,12 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
         for (int j = wg; j < n; j += 2) {
             const int t0 = tl.tile(tile0 + j) * kTileTokens;
             // (a warp that gives up stays until the stream's vote: the others may have seen the tile arrive)
-            bad = !tc::mbar_wait(&s_full[wg], (j >> 1) & 1, abort_flag, wlim) || (HOOK && a.stall == kStallWarp && j == 0 && warp == 0);
-            tc::tc_fence_after();
+            bad = !tc::mbar_wait(&k_seen[wg], (j >> 1) & 1, abort_flag, wlim);
             const int good = pok[j % C::NSC];
             const bool full = good == 3 && t0 + kTileTokens <= all_end && (t0 >= all_lo || t0 + kTileTokens <= a.sinks);
+            const uint32_t zeros = live ? put_part(j, t0, good, full) : 0u;
+            if (!tc::mbar_wait(&s_full[wg], (j >> 1) & 1, abort_flag, wlim) || (HOOK && a.stall == kStallWarp && j == 0 && warp == 0)) bad = true;
+            tc::tc_fence_after();
             // Value columns of tokens that no row sees are zeroed: their bytes may be anything (a NaN code
             // among them), and 0 times NaN is NaN.  One channel per thread of the stream's first half.
             if (!full && half == 0) {
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, D>::THREADS, 1) decode_fp8_wide_k
                 tc::fence_proxy_async_smem();
             }
             if (live) {
-                bad = full ? !tile(std::true_type{}, j, t0, good) : !tile(std::false_type{}, j, t0, good);
+                bad = full ? !tile(std::true_type{}, j, t0, good, zeros) : !tile(std::false_type{}, j, t0, good, zeros);
             } else if (!bad) {
                 arrive(0);
                 arrive(1);
