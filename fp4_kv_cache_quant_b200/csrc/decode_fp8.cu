@@ -632,7 +632,7 @@ inline int64_t most_tiles(int64_t N, int T_q, int G, int rows, int window, int s
     // the group's query tokens: their windows span window + span - 1 tokens from any slot on
     const int64_t span = std::min<int64_t>(T_q, (rows - 1) / G + 2);
     const int64_t win = (window + span - 1 + kTileTokens - 2) / kTileTokens + 1;
-    return std::min(all, win + (sinks + kTileTokens - 1) / kTileTokens);
+    return std::min(all, win + ((int64_t)sinks + kTileTokens - 1) / kTileTokens);
 }
 
 template <int D>

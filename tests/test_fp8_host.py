@@ -166,3 +166,17 @@ def test_wait_test_hook(lib):
         return lib.bdfp8_debug_decode_wait_test(*[a[k] for k in a], None, limit, stall, None)
     assert call(limit=0) == -1 and call(stall=3) == -1 and call(stall=-1) == -1 and call(q=None) == -1
     assert call(B=0) == 0
+
+
+@pytest.mark.parametrize("sinks", [2 ** 31 - 1, 2 ** 31 - 127, 2 ** 31 - 128])
+def test_first_tokens_without_end(lib, sinks):
+    """Any count of first tokens: they are those of the table at the most, in the plan and the workspace as in the decode."""
+    mp = 64   # 4096 tokens, 32 tiles
+    want = bdfp8.bdfp8_decode_workspace_size(2, 1, 8, 2, 128, mp, 2, window=100, sinks=mp * 64)
+    assert want == bdfp8.bdfp8_decode_workspace_size(2, 1, 8, 2, 128, mp, 2) > 0
+    assert bdfp8.bdfp8_decode_workspace_size(2, 1, 8, 2, 128, mp, 2, window=100, sinks=sinks) == want
+    lens = [4096, 2000]
+    assert bdfp8.bdfp8_decode_plan(lens, 1, 8, 2, 128, 148, window=100, sinks=sinks) == \
+        bdfp8.bdfp8_decode_plan(lens, 1, 8, 2, 128, 148, window=100, sinks=4096)
+    # the decode, which asks for the same workspace, refuses one byte less before a launch
+    assert _decode(lib, mp=mp, w=100, s=sinks, ws=A, wb=want - 1) == -6
