@@ -103,9 +103,12 @@ def bdfp8_append(k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, seq_
     """Append the rows k, v [T, H_kv, d] of B sequences (rows cu_tokens[b] ..
     cu_tokens[b + 1] - 1 each; seq_lens counts them), rotating keys and, into q_out,
     queries q [T, H_q, d] by cos_sin [max_pos, rot_dim] (None: no rotation);
-    interleaved pairs adjacent elements (bdfp8_append in bdfp8.h).  Returns q_out."""
+    interleaved pairs adjacent elements (bdfp8_append in bdfp8.h).  Returns q_out, which
+    is allocated on `stream` where it is not given (rows of no sequence are not written)."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        # from the pool of the stream that writes it
+        with torch.cuda.stream(stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     rc = (_py or _calls()).append(
         k, v, cu_tokens, seq_lens, block_table, cos_sin, cache.k_pages, cache.v_pages, cache.kv_scales, cache.num_pages,
         cache.H_kv, cache.d, cache.fmt, open_blocks.k_open, open_blocks.v_open, q, q_out, positions,
