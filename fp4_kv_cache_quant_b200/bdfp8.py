@@ -49,7 +49,11 @@ def load() -> ctypes.CDLL:
         L.bdfp8_debug_decode_wait_test.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i64, i, i, i, f, i, p, sz, p, p,
                                                    ctypes.c_longlong, i, p]
         L.bdfp8_debug_decode_wait_test.restype = i
-        from . import _bdfp8_py
+        try:
+            from . import _bdfp8_py
+        except ImportError as e:
+            raise OSError("the extension module of the 8-bit cache's calls is missing or does not load: build it with "
+                          f"`python -m fp4_kv_cache_quant_b200.build` (g++, Python's and torch's headers): {e}") from e
         _bdfp8_py.set_error(BDFP4Error)
         _lib, _py = L, _bdfp8_py
     return _lib

@@ -4,7 +4,8 @@ Each translation unit compiles to an object of its own, in parallel (one nvcc
 process per .cu file, under _build/ beside this file), and nvcc links them
 into the shared library.  The Python side of the 8-bit cache's calls
 (csrc/py_bdfp8.cpp, an extension module against this interpreter and torch)
-compiles beside them and links to that library."""
+compiles beside them and links to that library; where its compiler or headers
+are missing the library is built all the same, with a warning."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -13,6 +14,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -36,11 +38,8 @@ def _headers() -> list[str]:
         glob.glob(os.path.join(HERE, "..", "include", "*.h"))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PY_LIB):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
-    return any(os.path.getmtime(p) > t for p in [*sources(), PY_SRC, *_headers()])
+def _stale(target: str, deps: list[str]) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in deps)
 
 
 def _compile_py(verbose: bool) -> tuple[str, str]:
@@ -67,6 +66,19 @@ def _link_py(obj: str) -> None:
     os.replace(PY_LIB + ".tmp", PY_LIB)
 
 
+def _build_py(compiled: concurrent.futures.Future, verbose: bool) -> None:
+    """The extension module, once the library stands."""
+    try:
+        obj, log = compiled.result()
+        if verbose and log.strip():
+            print(log, end="", flush=True)
+        _link_py(obj)
+    except (ImportError, OSError, RuntimeError, subprocess.CalledProcessError) as e:
+        if os.path.exists(PY_LIB):
+            os.remove(PY_LIB)   # of older sources: its calls need not be this library's
+        warnings.warn(f"the 8-bit cache's Python calls are not built: {e}", RuntimeWarning, stacklevel=3)
+
+
 def _compile(src: str, extra: list[str], verbose: bool) -> tuple[str, str]:
     obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
     cmd = [NVCC, *FLAGS, *extra, "-c", "-o", obj, src]
@@ -81,23 +93,27 @@ def _compile(src: str, extra: list[str], verbose: bool) -> tuple[str, str]:
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None, out: str | None = None) -> str:
     """Compile csrc/*.cu into libbdfp4.so (or `out`; then without the extension module) unless it is up to date."""
     target = out or LIB
-    if not force and out is None and not _stale():
+    headers = _headers()
+    lib = force or out is not None or _stale(LIB, [*sources(), *headers])
+    py = out is None and (force or _stale(PY_LIB, [PY_SRC, *headers]))
+    if not lib and not py:
         return LIB
     os.makedirs(OBJ, exist_ok=True)
-    srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
-        py = ex.submit(_compile_py, verbose) if out is None else None
+    srcs = sources() if lib else []
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + py, os.cpu_count() or 1))) as ex:
+        ext = ex.submit(_compile_py, verbose) if py else None
         results = list(ex.map(lambda s: _compile(s, extra or [], verbose), srcs))
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log, end="", flush=True)
-    soname = ["-Xlinker", "-soname=" + os.path.basename(LIB)]   # what the extension module looks for beside it
-    cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *soname, "-o", target + ".tmp", *[o for o, _ in results]]
-    subprocess.run(cmd, check=True)
-    os.replace(target + ".tmp", target)
-    if py is not None:
-        _link_py(py.result()[0])
+    if lib:
+        soname = ["-Xlinker", "-soname=" + os.path.basename(LIB)]   # what the extension module looks for beside it
+        cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *soname, "-o", target + ".tmp", *[o for o, _ in results]]
+        subprocess.run(cmd, check=True)
+        os.replace(target + ".tmp", target)
+    if ext is not None:
+        _build_py(ext, verbose)
     return target
 
 
