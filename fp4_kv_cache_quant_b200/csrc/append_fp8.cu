@@ -108,20 +108,12 @@ struct Unit {
     }
 };
 
-// A unit's cosines and sines: of row `cs` of the table (rot / 2 cosines, then as many sines), or 1 and 0 (cs = null).
+// A unit's cosines and sines, of row `cs` of the table (rot / 2 cosines, then as many sines).
 struct Turn {
     float c[8], s[8];
     __device__ __forceinline__ void load(const float* cs, int u, int rot) {
-        if (cs) {
-            load8(cs + 8 * u, c);
-            load8(cs + (rot >> 1) + 8 * u, s);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 1.0f;
-                s[i] = 0.0f;
-            }
-        }
+        load8(cs + 8 * u, c);
+        load8(cs + (rot >> 1) + 8 * u, s);
     }
     // the unit's elements a[8], b[8]
     template <bool EXACT, bool ADJ>
@@ -197,9 +189,8 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     const int mine = blk0 + item - ((c0 >> 4) + 2 * b);
     if (mine < blk0 || mine > last) return;
 
-    // table row of token t's position (null: not rotated)
+    // table row of token t's position (null: none; the token stays as it is, infinities and signs of zeros too)
     auto angles = [&](int t, int index) -> const float* {
-        if (a.rot == 0) return nullptr;
         const int pos = a.positions ? a.positions[t] : index;
         if (pos < 0 || pos >= a.max_pos) {
             set_status(a.dev_status, BDFP8_DEV_BAD_POSITION);
@@ -212,11 +203,15 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
     // of every other query head of the group, so cosines and sines are loaded once per thread.
     const int tok = tid / UNITS % kBlockTokens, side = tid / D;
     const Unit un(tid % UNITS, a.rot, ADJ);
-    const bool turns = 16 * un.u < a.rot;
     const int my = mine * kBlockTokens + tok;                    // its index in the sequence
     const bool live = my >= start && my < end;
     Turn tn;
-    if (turns && live) tn.load(angles(c0 + my - start, my), un.u, a.rot);
+    bool turns = false;
+    if (16 * un.u < a.rot && live)
+        if (const float* const cs = angles(c0 + my - start, my)) {
+            turns = true;
+            tn.load(cs, un.u, a.rot);
+        }
 
     const bool reads_open = start % kBlockTokens != 0;
     const bool chained = reads_open && last != blk0;
@@ -267,14 +262,12 @@ __global__ void __launch_bounds__(2 * D, 384 / D) append_fp8_kernel(const Append
                         const uint4 w1 = *reinterpret_cast<const uint4*>(row + un.eb);
                         unpack8(w0, x);
                         unpack8(w1, x + 8);
-                        if (turns) {
-                            if (blk == mine) {
-                                tn.apply<true, ADJ>(x, x + 8);
-                            } else {
-                                Turn other;
-                                other.load(angles(t, i), un.u, a.rot);
-                                other.apply<true, ADJ>(x, x + 8);
-                            }
+                        if (blk == mine) {
+                            if (turns) tn.apply<true, ADJ>(x, x + 8);
+                        } else if (const float* const cs = 16 * un.u < a.rot ? angles(t, i) : nullptr) {
+                            Turn other;
+                            other.load(cs, un.u, a.rot);
+                            other.apply<true, ADJ>(x, x + 8);
                         }
                         if (blk == last) {
                             store8(open + un.ea, x);

@@ -37,3 +37,33 @@ def test_append_on_a_given_stream(given):
     if not given:
         at = [s for s in torch.cuda.memory_snapshot() if s["address"] <= got.data_ptr() < s["address"] + s["total_size"]]
         assert len(at) == 1 and at[0]["stream"] == st.cuda_stream
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_tokens_of_a_bad_position_stay_as_they_are(interleaved):
+    """Unrotated to the bit: infinities do not reach the elements they would be paired with, zeros keep their signs."""
+    lp = Loop(1, 1, 2, 64, bdfp8.E4M3, 64, interleaved, seed=82)
+    g = torch.Generator().manual_seed(83)
+    k, v, q = (torch.randn((40, h, 64), generator=g).bfloat16() for h in (1, 1, 2))
+    q[3, 0, 1], q[3, 1, 40], q[5, 0, 0] = float("inf"), float("-inf"), float("nan")
+    q[4, :, ::3], k[4, :, ::3], k[20, :, 1::2] = -0.0, -0.0, -0.0
+    pos = torch.arange(40, dtype=torch.int32)
+    bad = [3, 4, 5, 20, 39]
+    pos[bad] = torch.tensor([-1, 512, 2 ** 31 - 1, -2 ** 31, 513], dtype=torch.int32)
+    st = _status()
+    got = bdfp8.bdfp8_append(k.cuda(), v.cuda(), _i32(0, 40), _i32(40), torch.from_numpy(lp.bt).cuda(),
+                             torch.from_numpy(lp.cs).cuda(), lp.cache, lp.open, q=q.cuda(), positions=pos.cuda(),
+                             interleaved=interleaved, dev_status=st)
+    assert int(st) == bdfp8.DEV_BAD_POSITION
+    same = lambda a, b: torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))  # noqa: E731
+    num = torch.tensor([i for i in range(64) if i != 0])
+    for t in bad:
+        assert same(got[t].cpu()[:, num], q[t][:, num])   # (a NaN's payload may change)
+    assert torch.isnan(got[5, 0, 0])
+    codes = ref.codes_of(lp.cache)[0][lp.bt[0, 0], 0]     # [64, 64]
+    for t in (4, 20):
+        zero = (k[t, 0] == 0).numpy()
+        assert zero.any() and np.all(codes[t][zero] == 0x80)
+    good = [t for t in range(40) if t not in bad]
+    want = ref.rotate(q[good].double().numpy(), lp.cs[good].astype(np.float64), interleaved)
+    assert np.all(np.abs(got[good].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 4.5 * 2.0 ** -24 * 6)
