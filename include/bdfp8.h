@@ -85,9 +85,10 @@ typedef enum { BDFP8_E4M3 = 0, BDFP8_E5M2 = 1 } bdfp8_fmt;
  * rows of its new tokens in the last block.  A sequence that starts at a whole
  * block (a new prompt) needs nothing in them.
  *
- * Errors on the device: cu_tokens out of order or seq_lens out of
+ * Errors on the device: cu_tokens out of order or out of [0, T] or seq_lens out of
  * [n, 64 max_pages_per_seq] (BDFP4_DEV_BAD_SEQLEN: the sequence is skipped,
- * its q_out rows too), a block_table entry out of range (BDFP4_DEV_BAD_PAGE: the block
+ * its q_out rows too; entries of cu_tokens that are not in order also leave it open
+ * which tokens of the call's other sequences are appended), a block_table entry out of range (BDFP4_DEV_BAD_PAGE: the block
  * is not written, its open rows are), a position out of range
  * (BDFP8_DEV_BAD_POSITION: the token counts as unrotated).  Sequences must not
  * share a page that the call writes.

@@ -67,3 +67,41 @@ def test_tokens_of_a_bad_position_stay_as_they_are(interleaved):
     good = [t for t in range(40) if t not in bad]
     want = ref.rotate(q[good].double().numpy(), lp.cs[good].astype(np.float64), interleaved)
     assert np.all(np.abs(got[good].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 4.5 * 2.0 ** -24 * 6)
+
+
+@pytest.mark.parametrize("B, swaps", [(4, [1]), (40, [3, 20, 39]), (200, [1, 100, 150, 199])])
+def test_sequences_out_of_order_are_reported_and_nothing_else_is_written(B, swaps):
+    """cu_tokens that falls: a block of any sequence is written as it should be, or not at all."""
+    r = np.random.default_rng(B)
+    new = r.integers(1, 60, B)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    for i in swaps:
+        cu[i] = r.integers(0, T + 40) if i % 2 else -5
+    lp = Loop(B, 1, 1, 64, bdfp8.E4M3, 0, False, mp=64, seed=84)
+    lens = np.array([max(cu[b + 1] - cu[b], 1) for b in range(B)], np.int32)
+    k = torch.randn((T, 1, 64), generator=torch.Generator().manual_seed(85)).bfloat16()
+    st = _status()
+    bdfp8.bdfp8_append(k.cuda(), k.cuda(), torch.from_numpy(cu).cuda(), torch.from_numpy(lens).cuda(), torch.from_numpy(lp.bt).cuda(),
+                       None, lp.cache, lp.open, dev_status=st)
+    assert int(st) == bdfp4.DEV_BAD_SEQLEN
+    kn = k.double().numpy()
+    K, V = ref.codes_of(lp.cache)
+    sc = lp.cache.kv_scales.cpu().numpy()
+    touched = np.zeros(sc.shape, bool)
+    written = 0
+    for b in range(B):
+        if 0 <= cu[b] <= cu[b + 1] <= T and lens[b] <= 64 * lp.bt.shape[1]:   # (a longer one is skipped, too)
+            lp.ref.append(b, kn[cu[b]: cu[b + 1]], kn[cu[b]: cu[b + 1]])
+        for i, (kc, ks), (vc, vs) in lp.ref.blocks(b):
+            pg, s = lp.bt[b, i // 4], i % 4
+            if sc[pg, 0, 0, s] == -7.0:
+                continue
+            written += 1
+            touched[pg, :, :, s] = True
+            at = slice(16 * s, 16 * s + 16)
+            assert np.array_equal(K[pg, :, at], kc) and np.array_equal(V[pg, :, at], vc)
+            assert np.array_equal(sc[pg, :, 0, s], ks) and np.array_equal(sc[pg, :, 1, s], vs)
+    assert written and np.all(sc[~touched] == -7.0)
+    left = np.repeat(~touched[:, :, 0], 16, axis=2)
+    assert np.all(K[left] == lp.canary) and np.all(V[left] == lp.canary)
