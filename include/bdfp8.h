@@ -133,7 +133,7 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * Arithmetic: a query row is split into two E4M3 terms, exact for a bf16 element
  * down to 2^-9 of the row's largest (2^-13 with up to 16 rows), to 2^-17 of the
  * largest below; logits, softmax and sums are fp32; a probability times its value
- * block's scale (rounded up to a power of two, 2^-96 at the least) goes into the value
+ * block's scale (rounded up to a power of two, 2^-92 at the least) goes into the value
  * product as three E5M2 terms: relative error 2^-9, a floor of 2^-28 of the largest such
  * product among the tokens of a split that the row sees.  (A token whose product is
  * below 2^-148 of that one's leaves the sum of probabilities too.)  A value block of
@@ -145,7 +145,8 @@ BDFP4_API size_t bdfp8_decode_workspace_size(int B, int T_q, int H_q, int H_kv, 
  * sets BDFP4_DEV_BAD_SEQLEN (rows at negative indexes see nothing), N_b outside
  * [0, 64 max_pages_per_seq] sets it and gives zeros.  chunk_tiles <= 0 plans
  * from max_pages_per_seq.  workspace as bdfp8_decode_workspace_size says (NULL
- * where that is 0), else BDFP4_ERR_WORKSPACE.
+ * where that is 0; what it says of chunk_tiles = 1 covers every plan), else
+ * BDFP4_ERR_WORKSPACE.
  */
 BDFP4_API int bdfp8_decode(const void* q, const void* k_pages, const void* v_pages, const float* kv_scales,
                            const int32_t* block_table, const int32_t* seq_lens, int B, int T_q, int H_q, int H_kv,

@@ -117,3 +117,17 @@ def test_a_captured_window_step(d, fmt):
         check(outs[0], qo[0].view(2, 1, 8, d).cpu(), lp.cache, lp.bt, [38 + s, 121 + s], 50, 3, scale=0.09)
     for name in ("k_pages", "v_pages", "kv_scales"):
         assert torch.equal(getattr(lp.cache, name), getattr(twin.cache, name))
+
+
+@FORMS
+@pytest.mark.parametrize("T, G", [(5, 2), (16, 1), (40, 4), (140, 1)])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (7, 2)])
+def test_sequences_shorter_than_their_query_tokens(T, G, d, fmt, window, sinks):
+    """Rows before the first token see nothing: zeros, and the length is reported."""
+    lens = [3, T - 1, T + 90, 0]
+    cache, bt = make_cache(lens, 2, d, fmt, 103, window, sinks, T)
+    q = queries(4, T, 2 * G, d, 104)
+    for chunk in (1, 2):
+        st = _status()
+        got = check(decode(q, cache, bt, lens, chunk, window, sinks, st), q, cache, bt, lens, window, sinks)
+        assert int(st) == bdfp4.DEV_BAD_SEQLEN and not got[0, : T - 3].any() and not got[3].any()
