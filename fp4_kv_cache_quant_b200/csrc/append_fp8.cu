@@ -9,7 +9,7 @@
 // token's cosines and sines for its key and half of the group's query heads (loaded for
 // each of them the kernel ran 143 M warp instructions for 32768 tokens at 32 / 8 heads,
 // 184 us).  Measured: those tokens 140 us, 5200 GB/s or 79 % of the copy rate, bound by
-// issue and loads in flight; 16 tokens 5.3 us a call.
+// issue and loads in flight; 16 tokens 5.2 us a call (4.8 in a captured graph).
 //
 // Which sequence a CTA serves: sequence b gets the item numbers f(b) .. f(b+1) - 1,
 // f(b) = cu[b] / 16 + 2 b.  n tokens from any offset touch at most n / 16 + 2 blocks

@@ -24,10 +24,14 @@
 //
 // Two blocks would do for the bandwidth; three of two 16 KB key and two value stages hide a
 // tile's chain (900 to 1000 ns alone: logits, maximum over four warps, probabilities,
-// value product) behind one another's.  Measured at 32 / 8 heads: 16 x 32768 tokens 167 us
-// (6440 GB/s, 98 % of the copy rate), 64 ragged contexts of 8 to 131 thousand 570 to 604, 1024
-// tokens of one sequence 5.9; 16 rows are bound by instruction issue, 690 ns a tile and
-// SM against 740 of memory.
+// value product) behind one another's.  Measured at 32 / 8 heads: 16 x 32768 tokens 168 us
+// (6410 GB/s; 154 to 159 as graph replays, above the copy rate of 6545, which writes
+// half), 64 ragged contexts of 8 to 131 thousand (32 / 4 heads) 577 to 606, 1024 tokens of
+// one sequence 5.9.  A tile fed from L2 takes an SM 381, 449 and 580 ns at 4, 8 and 16 rows,
+// memory 741 at d = 128 and 371 at d = 64: so d = 64 is bound by the softmax's instructions, and
+// 16 rows at d = 128 (16 sequences of 20 to 33 thousand tokens 176 us, 157 to 165 as graph
+// replays, 125 at the copy rate) by how well two blocks an SM and 256 uneven blocks in
+// 296 places keep the memory busy.
 //
 // A row group's tiles are those of the first `sinks` tokens and those from its oldest
 // window token on, numbered one after another and cut into splits, so a window
@@ -731,7 +735,9 @@ static bool merges_in_cluster(int rows, int max_splits, int64_t ctas, int sms) {
 // lengths), up to 21 splits each: the split count of least modelled time, which is the plan, takes 1% more than
 // the fastest split on average and 23% at worst.  Measured, us, by tiles a split: 131072 tokens, 8 KV heads, 4 rows
 // 128: 112, 64: 61, 32: 48, 16: 56; one KV head 128: 115, 64: 61, 32: 34, 16: 22; 4 x 4096 tokens 32: 30, 8: 12, 4:
-// 13, 1: 19; 64 x 1000 ragged tokens 8: 22, 4: 27, 2: 35.  tiles_of(b): the tiles that a row group of sequence
+// 13, 1: 19; 64 x 1000 ragged tokens 8: 22, 4: 27, 2: 35.  The block times are the fit's: 16 rows have come
+// down since, and the one for 128-row groups stands for a few live rows as for all (1210 and 1480 ns a tile fed
+// from L2, start left out).  tiles_of(b): the tiles that a row group of sequence
 // b sees at most.
 template <class TilesOf>
 static int plan(int B, const TilesOf& tiles_of, int64_t items, int sms, int rows, int d) {

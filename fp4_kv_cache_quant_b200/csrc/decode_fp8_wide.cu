@@ -5,9 +5,10 @@
 // M = 128 query rows and N = 128 tokens, O = P V with N = D channels, so a TMEM lane
 // and its threads own a whole row: sums need no exchange between threads, a maximum
 // one between two, and a row's probabilities go back into TMEM, where the value
-// product reads them as its A operand.  Its time for a tile is the same for one row
-// and for 128 (1315 ns); the transposed form pays by the row (441, 520 and 690 ns at
-// 4, 8 and 16 rows, 1380 at 32).
+// product reads them as its A operand.  Its time for a tile fed from L2 hardly depends on
+// the rows (1210 ns at 17 and 32, 1480 at 64 and 128; 1240 and 1380 at d = 64); the
+// transposed form pays by the row (381, 449 and 580 ns at 4, 8 and 16 rows; 1380 at 32 in an
+// earlier state of both).
 // Both q terms add into one S (q2 at q1's scale: an absolute error of 2^-17 of the
 // row's largest element at the most), the three E5M2 terms of p c into one O.
 //
@@ -19,9 +20,13 @@
 // (the probabilities over them: 32 tokens' logits read free 32 columns, their terms
 // take 24) and two O, 512 columns at D = 128.  (With the probabilities in shared memory
 // a stream's next logits need not wait for its value product, but the stores wait
-// behind the operand reads: 1830 ns a tile.)  What bounds it: the thread that issues
-// the MMAs.  A tile is 20 of them at 67 cycles (two terms of q, three of p c), beside
-// seven waits and commits of 100 to 200 cycles each.
+// behind the operand reads: 1830 ns a tile against 1315.)  What bounds it: the chain of a
+// stream (logits, maximum, exponentials, terms, value product), which the other stream
+// covers in part, and the thread that issues the MMAs: a tile is 20 of them at 67 cycles
+// (two terms of q, three of p c), beside seven waits and commits of 100 to 200 cycles
+// each.  Up to 32 rows all live warps stand on one scheduler, so that every instruction of
+// the chain counts: 16 x 32768 tokens, 32 / 4 heads: 172 us at 17 and 32 rows (82 at the
+// copy rate), 214 at 128.
 
 #include "decode_fp8.cuh"
 
