@@ -126,11 +126,11 @@ __device__ __forceinline__ void put_query(uint8_t* op, int row, int lane, uint32
 constexpr float kRise = 4.0f;
 constexpr int kTopExp = 11, kLift = 22;
 
-// e and 2^(-e - kLift) of a scale.  e >= -92, as sums of w 2^-e over 2^30 tokens have to stay finite (a scale below, 0
+// e and 2^(-e - kLift) of a scale (of its amount: -0 is 0).  e >= -92, as sums of w 2^-e over 2^30 tokens have to stay finite (a scale below, 0
 // among them, gives r < 1/2); the other is down to 2^-149, which fp32 holds.  A scale that is no number gets finite
 // ones: its r is none.
 __device__ __forceinline__ void scale_parts(float c, float& e, float& down) {
-    const uint32_t u = min(max((__float_as_uint(c) + 0x7fffffu) >> 23, 127u - 92u), 254u);
+    const uint32_t u = min(max((__float_as_uint(fabsf(c)) + 0x7fffffu) >> 23, 127u - 92u), 254u);
     e = __uint_as_float(0x4b000000u + u) - (8388608.0f + 127.0f);
     down = __uint_as_float(max((254u - u) << 23, 0x400000u)) * (1.0f / (float)(1 << kLift));
 }

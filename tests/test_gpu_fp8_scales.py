@@ -225,3 +225,18 @@ def test_nothing_but_zeros(G):
     cache, bt = appended([300], 1, 128, bdfp8.E4M3, 1.0, [[(0, 300)]], False, 76)
     got = decode(queries(1, 2, G, 128, 77), cache, bt, [300], 1)
     assert not got.any()
+
+
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+@pytest.mark.parametrize("d, fmt", FORMS)
+@pytest.mark.parametrize("T, G", [(1, 4), (1, 16), (3, 2), (1, 24), (3, 40)])
+def test_scales_of_zero(T, G, d, fmt, zero):
+    """Blocks whose value scale is a zero of either sign give nothing and cost nothing."""
+    lens = [300, 40]
+    cache, bt = make_cache(lens, 2, d, fmt, 78)
+    cache.kv_scales[:, :, 1] *= 2.0 ** -20
+    for b, page, blk in ((0, 0, 1), (0, 4, 0), (1, 0, 2)):
+        cache.kv_scales[int(bt[b, page]), :, 1, blk] = zero
+    q = queries(2, T, 2 * G, d, 79)
+    for chunk in (1, 2):
+        check(decode(q, cache, bt, lens, chunk), q, cache, bt, lens)

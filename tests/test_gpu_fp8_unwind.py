@@ -41,3 +41,14 @@ def test_a_wait_that_runs_out_unwinds_and_reports(T, G, chunk):
             assert int(st) == bdfp4.DEV_TIMEOUT
         st.zero_()
         assert torch.equal(decode(q, cache, bt, lens, chunk, status=st), before) and int(st) == 0
+
+
+@pytest.mark.parametrize("T, G, d, fmt", [(1, 4, 128, bdfp8.E4M3), (2, 4, 128, bdfp8.E4M3), (1, 16, 128, bdfp8.E4M3),
+                                          (1, 8, 64, bdfp8.E4M3), (1, 8, 128, bdfp8.E5M2), (1, 24, 64, bdfp8.E5M2)])
+def test_the_hook_refuses_other_shapes(T, G, d, fmt):
+    cache, bt = make_cache([64], 1, d, fmt, 52)
+    q = queries(1, T, G, d, 53).cuda()
+    sl = torch.tensor([64], dtype=torch.int32, device="cuda")
+    with pytest.raises(bdfp4.BDFP4Error, match="compiled set"):
+        bdfp8.bdfp8_debug_decode_wait_test(q, cache, torch.from_numpy(bt).cuda(), sl, 0.1, 1, None, torch.empty_like(q), SHORT_WAIT,
+                                           bdfp8.STALL_TILE)
